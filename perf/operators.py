@@ -1,0 +1,467 @@
+"""Cases of the block norms and of the products with 4-bit expert weights: inputs, plain forms, exact values and the
+framework's calls.
+
+Five operators, in the notation of include/moe.h:
+
+  block norm           out = rs * x + bs * a(gate) * N(y; post_gain),  h = N(out; next_gain)
+                       N(v; g) = g * v / sqrt(mean(v^2) + eps); y is the block's output or the weighted sum of a
+                       token's expert rows; without y only h = N(x; next_gain) is computed
+  block norm backward  dx, dy, the gains' gradients and the gate's from the gradients of out and h
+  4-bit round trip     W -> 4-bit codes q and group scales s -> s * (q - 8)
+  4-bit matvec         y[t] = W x[t]
+  4-bit grouped FFN    y[r] = Wd[e] (silu(Wg[e] x[row r]) * (Wu[e] x[row r])), rows grouped by expert e
+
+A 4-bit matrix W [R, C] stands for W[r, c] = s[r, c // group] * (q[r, c] - 8) with q in 0..15 and s in bf16.
+"""
+import math
+
+import torch
+
+own = False
+
+DEV = "cuda"
+DT = {"bf16": torch.bfloat16, "fp32": torch.float32}
+EPS = 1e-6
+
+
+# ---- cases ------------------------------------------------------------------
+
+def listed():
+    return [
+        # one token between two blocks of the page's model (hidden 6,144): latency only
+        dict(name="norm_token", op="norm", T=1, d=6144, dtype="bf16", branch="y", post=True, gate=0, act="none",
+             next=True),
+        # a decode step's block end: each token's eight expert rows weighted and summed, normed, gated by one learned
+        # vector, added to the residual, and the next block's norm
+        dict(name="norm_combine_64", op="norm", T=64, d=6144, dtype="bf16", branch="perm8", post=True, gate=64,
+             act="none", next=True),
+        # a long pre-training sequence through the same block end, the block's output already summed
+        dict(name="norm_seq32k", op="norm", T=32768, d=6144, dtype="bf16", branch="y", post=True, gate=4096,
+             act="tanh", next=True),
+        # the first norm of a stack on a small float32 layer: no branch, odd row count
+        dict(name="norm_first_fp32", op="norm", T=4093, d=1088, dtype="fp32", branch="none", post=False, gate=0,
+             act="none", next=True),
+        # training backward at the page's width, one gate vector a sequence
+        dict(name="norm_bwd_seq16k", op="norm_bwd", T=16384, d=6144, dtype="bf16", branch="y", post=True, gate=2048,
+             act="tanh", next=True),
+        # a small float32 layer's backward with one gate row a token (a projection of the block's input)
+        dict(name="norm_bwd_token_gate_fp32", op="norm_bwd", T=1021, d=1024, dtype="fp32", branch="y", post=True,
+             gate=1, act="sigmoid", next=True),
+        # four experts' gate projections made 4-bit when a checkpoint is loaded
+        dict(name="w4_quantize_experts", op="quant", n=4, R=1792, C=6144, group=128, dtype="bf16"),
+        # one small float32 matrix, finest groups, odd row count
+        dict(name="w4_quantize_fp32", op="quant", n=1, R=515, C=1024, group=32, dtype="fp32"),
+        # one token through one projection
+        dict(name="w4_matvec_token", op="matvec", T=1, C=6144, R=6144, group=128, dtype="bf16"),
+        # a small odd batch through an expert's gate projection, finest groups
+        dict(name="w4_matvec_19", op="matvec", T=19, C=6144, R=1792, group=32, dtype="bf16"),
+        # one token of a decode step on one expert-parallel rank (96 local experts, top-8)
+        dict(name="w4_ffn_token", op="ffn", T=1, d=6144, F=1792, E=96, k=8, group=128, dtype="bf16"),
+        # a decode batch: 512 rows, nearly every expert has a few
+        dict(name="w4_ffn_64", op="ffn", T=64, d=6144, F=1792, E=96, k=8, group=128, dtype="bf16"),
+    ]
+
+
+def _log(rng, lo, hi):
+    return min(hi, max(lo, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+
+
+def draw(rng):
+    op = rng.choice(["norm", "norm", "norm_bwd", "norm_bwd", "quant", "matvec", "ffn", "ffn"])
+    if op in ("norm", "norm_bwd"):
+        d = 64 * _log(rng, 1, 128)
+        top = 32768 if op == "norm" else 16384
+        T = _log(rng, 1, max(1, min(200000, top * 6144 // d // 2)))
+        branch = rng.choice(["y", "y", "y", "none"] if op == "norm_bwd" else ["y", "y", "perm", "none"])
+        if branch == "perm":
+            k = rng.choice([1, 2, 3, 4, 6, 8])
+            T = max(1, T // (k + 1))
+            branch = "perm%d" % k
+        has = branch != "none"
+        gate = rng.choice([0, 1, T, _log(rng, 1, T)]) if has else 0
+        return dict(op=op, T=T, d=d, dtype=rng.choice(["bf16", "bf16", "fp32"]), branch=branch,
+                    post=has and rng.random() < 0.8, gate=gate,
+                    act=rng.choice(["none", "sigmoid", "tanh"]) if gate else "none",
+                    next=not has or rng.random() < 0.75)
+    group = rng.choice([32, 64, 128])
+    if op == "quant":
+        C = 32 * _log(rng, 1, 192)
+        R = _log(rng, 1, 1792)
+        return dict(op=op, n=_log(rng, 1, 4), R=R, C=C, group=group, dtype=rng.choice(["bf16", "fp32"]))
+    if op == "matvec":
+        return dict(op=op, T=_log(rng, 1, 96), C=32 * _log(rng, 1, 192), R=_log(rng, 1, 6144), group=group,
+                    dtype=rng.choice(["bf16", "bf16", "fp32"]))
+    E = _log(rng, 1, 96)
+    return dict(op=op, T=_log(rng, 1, 64), d=64 * _log(rng, 1, 96), F=64 * _log(rng, 1, 28), E=E,
+                k=rng.randint(1, min(8, E)), group=group, dtype=rng.choice(["bf16", "bf16", "fp32"]))
+
+
+# ---- inputs -----------------------------------------------------------------
+
+def _norm_inputs(c, g):
+    T, d, dt = c["T"], c["d"], DT[c["dtype"]]
+
+    def rnd(*shape, std=1.0):
+        return torch.randn(*shape, generator=g, device=DEV) * std
+
+    v = {"x": None, "y": None, "y_perm": None, "slot_row": None, "topk_w": None, "post_gain": None, "gate": None,
+         "next_gain": None, "rs": 1.0, "bs": 1.0}
+    # a residual stream: a few channels much larger than the others
+    chan = 1.0 + 6.0 * (torch.rand(d, generator=g, device=DEV) < 0.01)
+    v["x"] = (rnd(T, d) * chan).to(dt)
+    if c["branch"] != "none":
+        v["bs"] = 0.7071
+        if c["branch"].startswith("perm"):
+            k = int(c["branch"][4:])
+            v["y_perm"] = rnd(T * k, d, std=0.3).to(dt)
+            v["slot_row"] = torch.randperm(T * k, generator=g, device=DEV).to(torch.int32).view(T, k)
+            if k > 1:  # one slot in sixteen belongs to an expert elsewhere
+                v["slot_row"] = torch.where(torch.rand(T, k, generator=g, device=DEV) < 1 / 16, -1, v["slot_row"])
+            w = torch.rand(T, k, generator=g, device=DEV) + 0.05
+            v["topk_w"] = w / w.sum(1, keepdim=True)
+        else:
+            v["y"] = rnd(T, d, std=0.3).to(dt)
+        if c["post"]:
+            v["post_gain"] = 1.0 + rnd(d, std=0.1)
+        if c["gate"]:
+            v["gate"] = rnd(-(-T // c["gate"]), d).to(dt)
+    if c["next"]:
+        v["next_gain"] = 1.0 + rnd(d, std=0.1)
+    if c["op"] == "norm_bwd":
+        v["d_out"] = rnd(T, d, std=0.02).to(dt)
+        v["dh"] = rnd(T, d, std=0.02).to(dt) if c["next"] else None
+        if c["branch"] != "none":
+            v["out"] = v.pop("x")  # the backward takes the forward's sum; x itself is not needed
+        else:
+            v["out"] = v.pop("x")
+    return v
+
+
+def _weights(g, n, R, C, group):
+    """Row-major codes (two a byte, the even column low) and scales of n matrices [R, C], as a checkpoint holds them."""
+    q = torch.randn(n, R, C, generator=g, device=DEV).mul_(2.3).round_().clamp_(-8, 7).add_(8).to(torch.uint8)
+    q = q[..., 0::2] | (q[..., 1::2] << 4)
+    s = (0.5 + torch.rand(n, R, -(-C // group), generator=g, device=DEV)) / (2.3 * math.sqrt(C))
+    return q, s.to(torch.bfloat16)
+
+
+def _inputs(c, seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    op, dt = c["op"], DT[c["dtype"]]
+    if op in ("norm", "norm_bwd"):
+        return _norm_inputs(c, g)
+    if op == "quant":
+        std = 1.0 / math.sqrt(c["C"])
+        return {"w": (torch.randn(c["n"], c["R"], c["C"], generator=g, device=DEV) * std).to(dt)}
+    if op == "matvec":
+        q, s = _weights(g, 1, c["R"], c["C"], c["group"])
+        return {"x": torch.randn(c["T"], c["C"], generator=g, device=DEV).to(dt), "q": q, "s": s}
+    T, d, F, E, k = c["T"], c["d"], c["F"], c["E"], c["k"]
+    v = {"x": torch.randn(T, d, generator=g, device=DEV).to(dt)}
+    for name, R, C in (("gate", F, d), ("up", F, d), ("down", d, F)):
+        v[name] = _weights(g, E, R, C, c["group"])
+    ids = torch.rand(T, E, generator=g, device=DEV).topk(k, dim=1).indices.reshape(-1)
+    order = torch.sort(ids, stable=True).indices
+    counts = torch.bincount(ids, minlength=E)
+    v["row_token"] = (order // k).to(torch.int32)
+    v["offsets"] = torch.cat([counts.new_zeros(1), counts.cumsum(0)]).to(torch.int32)
+    # which experts have rows, and where each row lies among its expert's: what a program that routes on the host knows
+    active = counts.nonzero()[:, 0]
+    where = torch.zeros(E, dtype=torch.int64, device=DEV)
+    where[active] = torch.arange(active.numel(), device=DEV)
+    expert = ids[order]
+    v["active"], v["row_expert"] = active, where[expert]
+    v["row_pos"] = torch.arange(T * k, device=DEV) - v["offsets"][expert].to(torch.int64)
+    v["most"] = int(counts.max())
+    return v
+
+
+def prepare(case, seed):
+    v = _inputs(case, seed)
+    v["case"] = case
+    if own:
+        from mixture_experts_layer_16_amd import binding as B
+        op = case["op"]
+        if op == "norm":
+            v["call"] = B.BlockNorm(v["x"], y=v["y"], y_perm=v["y_perm"], slot_row=v["slot_row"], topk_w=v["topk_w"],
+                                    post_gain=v["post_gain"], gate=v["gate"], gate_rows=case["gate"],
+                                    gate_act=case["act"], next_gain=v["next_gain"], res_scale=v["rs"],
+                                    branch_scale=v["bs"], eps=EPS)
+        elif op == "norm_bwd":
+            v["call"] = B.BlockNormBackward(d_out=v["d_out"], dh=v["dh"], out=v["out"], y=v["y"],
+                                            post_gain=v["post_gain"], gate=v["gate"], gate_rows=case["gate"],
+                                            gate_act=case["act"], next_gain=v["next_gain"], res_scale=v["rs"],
+                                            branch_scale=v["bs"], eps=EPS)
+        elif op == "quant":
+            v["call"] = B.W4Quantize(v["w"], group=case["group"])
+            v["values"] = torch.empty_like(v["w"])
+        elif op == "matvec":
+            v["call"] = B.W4Matvec(v["x"], B.w4_pack(v["q"], v["s"], group=case["group"]))
+        else:
+            w = [B.w4_pack(*v[name], group=case["group"]) for name in ("gate", "up", "down")]
+            v["call"] = B.W4GroupedFfn(v["x"], v["offsets"], *w, a_rows=v["row_token"])
+    return v
+
+
+# ---- one pass ---------------------------------------------------------------
+
+def run(state):
+    op = state["case"]["op"]
+    if own:
+        if op == "norm":
+            n = state["call"]()
+            return {"out": n.out, "h": n.h}
+        if op == "norm_bwd":
+            b = state["call"]()
+            return {"dx": b.dx, "dy": b.dy, "d_post_gain": b.d_post_gain, "dgate": b.dgate,
+                    "d_next_gain": b.d_next_gain}
+        if op == "quant":
+            return {"w": state["call"]().dequantize(out=state["values"])}
+        return {"y": state["call"]()}
+    return {"norm": _norm, "norm_bwd": _norm_bwd, "quant": _quant, "matvec": _matvec, "ffn": _ffn}[op](state)
+
+
+def _act(gate, act):
+    v = gate.float()
+    return torch.sigmoid(v) if act == "sigmoid" else torch.tanh(v) if act == "tanh" else v
+
+
+def _rows(table, T, period):
+    """Row t of the result: row t // period of the table."""
+    return table if table.shape[0] == T else table[torch.arange(T, device=table.device) // period]
+
+
+def _norm(s):
+    c, x = s["case"], s["x"].float()
+    dt = s["x"].dtype
+    out = x
+    if c["branch"] != "none":
+        if s["y"] is not None:
+            y = s["y"].float()
+        else:
+            row = s["slot_row"].long()
+            y = (s["y_perm"][row.clamp(min=0)].float() * (s["topk_w"] * (row >= 0))[..., None]).sum(1)
+        if s["post_gain"] is not None:
+            y = y * torch.rsqrt((y * y).mean(1, keepdim=True) + EPS) * s["post_gain"]
+        if s["gate"] is not None:
+            y = y * _rows(_act(s["gate"], c["act"]), c["T"], c["gate"])
+        out = s["rs"] * x + s["bs"] * y
+    h = None
+    if s["next_gain"] is not None:
+        h = (out * torch.rsqrt((out * out).mean(1, keepdim=True) + EPS) * s["next_gain"]).to(dt)
+    return {"out": out.to(dt) if c["branch"] != "none" else None, "h": h}
+
+
+def _norm_bwd(s):
+    c, dt, T = s["case"], s["out"].dtype, s["case"]["T"]
+    D = s["d_out"].float()
+    r = {"dx": None, "dy": None, "d_post_gain": None, "dgate": None, "d_next_gain": None}
+    if s["dh"] is not None:
+        o, dh = s["out"].float(), s["dh"].float()
+        rstd = torch.rsqrt((o * o).mean(1, keepdim=True) + EPS)
+        o = o * rstd
+        r["d_next_gain"] = (dh * o).sum(0)
+        u = dh * s["next_gain"]
+        D = D + rstd * (u - o * (u * o).mean(1, keepdim=True))
+    r["dx"] = (s["rs"] * D).to(dt)
+    if s["y"] is None:
+        return r
+    y = s["y"].float()
+    n, dn = y, s["bs"] * D
+    if s["post_gain"] is not None:
+        rstd = torch.rsqrt((y * y).mean(1, keepdim=True) + EPS)
+        y = y * rstd
+        n = y * s["post_gain"]
+    if s["gate"] is not None:
+        a = _act(s["gate"], c["act"])
+        slope = a * (1 - a) if c["act"] == "sigmoid" else 1 - a * a if c["act"] == "tanh" else torch.ones_like(a)
+        each = dn * n * _rows(slope, T, c["gate"])
+        if c["gate"] == 1:
+            r["dgate"] = each.to(dt)
+        else:
+            groups, whole = s["gate"].shape[0], T // c["gate"]
+            head = each[:whole * c["gate"]].view(whole, c["gate"], c["d"]).sum(1)
+            r["dgate"] = head if whole == groups else torch.cat([head, each[whole * c["gate"]:].sum(0, keepdim=True)])
+        dn = dn * _rows(a, T, c["gate"])
+    if s["post_gain"] is not None:
+        r["d_post_gain"] = (dn * y).sum(0)
+        u = dn * s["post_gain"]
+        dn = rstd * (u - y * (u * y).mean(1, keepdim=True))
+    r["dy"] = dn.to(dt)
+    return r
+
+
+def _quant(s):
+    w, group = s["w"].float(), s["case"]["group"]
+    n, R, C = w.shape
+    w = torch.nn.functional.pad(w, (0, -C % group)).view(n, R, -1, group)
+    scale = (w.abs().amax(3, keepdim=True) / 7).to(torch.bfloat16).float()
+    # in 64 bits: quotients next to a half fall on their own side of it
+    q = torch.where(scale > 0, w.double() / scale.double(), 0.0).round().clamp(-8, 7).float()
+    return {"w": (q * scale).view(n, R, -1)[..., :C].to(s["w"].dtype)}
+
+
+def _dequant(q, s, C, group):
+    q = torch.stack([q & 15, q >> 4], -1).flatten(-2)
+    return (q.float() - 8) * s.float().repeat_interleave(group, -1)[..., :C]
+
+
+def _matvec(s):
+    c = s["case"]
+    w = _dequant(s["q"][0], s["s"][0], c["C"], c["group"])
+    return {"y": (s["x"].float() @ w.t()).to(s["x"].dtype)}
+
+
+def _ffn(s):
+    c, act = s["case"], s["active"]
+    wg, wu = (_dequant(s[n][0][act], s[n][1][act], c["d"], c["group"]) for n in ("gate", "up"))
+    wd = _dequant(s["down"][0][act], s["down"][1][act], c["F"], c["group"])
+    x = torch.zeros(act.numel(), s["most"], c["d"], device=s["x"].device)  # each expert's rows, padded to the longest
+    at = (s["row_expert"], s["row_pos"])
+    x[at] = s["x"].float()[s["row_token"].long()]
+    g = torch.bmm(x, wg.transpose(1, 2).contiguous())
+    h = g / (1 + torch.exp(-g)) * torch.bmm(x, wu.transpose(1, 2).contiguous())
+    return {"y": torch.bmm(h, wd.transpose(1, 2).contiguous())[at].to(s["x"].dtype)}
+
+
+# ---- what a pass cannot do without ------------------------------------------
+
+def work(case):
+    c = case
+    es = 2 if c["dtype"] == "bf16" else 4
+    if c["op"] in ("norm", "norm_bwd"):
+        T, d = c["T"], c["d"]
+        groups = -(-T // c["gate"]) if c["gate"] else 0
+        gains = 4 * d * (int(c["post"]) + int(c["next"]))
+        if c["op"] == "norm":
+            rows = {"none": 0, "y": 1}.get(c["branch"], int(c["branch"][4:] or 0) if c["branch"][:4] == "perm" else 0)
+            tensors = 1 + rows + (c["branch"] != "none") + int(c["next"])
+            idx = 8 * T * rows if c["branch"].startswith("perm") else 0
+            return {"bytes": es * d * (T * tensors + groups) + gains + idx, "flops": T * d * (6 * tensors)}
+        has = c["branch"] != "none"
+        tensors = 2 + 2 * int(c["next"]) + 2 * has  # d_out, dx; out, dh; y, dy
+        dgate = groups * d * (es if c["gate"] == 1 else 4)
+        return {"bytes": es * d * (T * tensors + groups) + 2 * gains + dgate, "flops": T * d * 8 * tensors}
+    if c["op"] == "quant":
+        n = c["n"] * c["R"] * c["C"]
+        groups = c["n"] * c["R"] * -(-c["C"] // c["group"])
+        return {"bytes": 2 * es * n + n // 2 + 2 * groups, "flops": 6 * n}
+    if c["op"] == "matvec":
+        n = c["R"] * c["C"]
+        return {"bytes": n // 2 + 2 * c["R"] * -(-c["C"] // c["group"]) + es * c["T"] * (c["C"] + c["R"]),
+                "flops": 2 * n * c["T"]}
+    T, d, F, E, k, grp = c["T"], c["d"], c["F"], c["E"], c["k"], c["group"]
+    active = E * (1 - (1 - k / E) ** T)
+    one = 2 * F * (d // 2 + 2 * -(-d // grp)) + d * (F // 2 + 2 * -(-F // grp))
+    return {"bytes": int(active * one) + es * (T * d + T * k * d) + 4 * (T * k + E + 1), "flops": 6 * T * k * d * F}
+
+
+# ---- the definitions in 64 bits ---------------------------------------------
+
+def exact(case, seed):
+    v = _inputs(case, seed)
+    f = {k: t.double() if isinstance(t, torch.Tensor) and t.is_floating_point() else t for k, t in v.items()}
+    return {"norm": _exact_norm, "norm_bwd": _exact_norm_bwd, "quant": _exact_quant, "matvec": _exact_matvec,
+            "ffn": _exact_ffn}[case["op"]](case, f)
+
+
+def _exact_gate(c, gate):
+    """(a(gate), a'(gate)) row by row of the tokens."""
+    a = 1 / (1 + torch.exp(-gate)) if c["act"] == "sigmoid" else torch.tanh(gate) if c["act"] == "tanh" else gate
+    p = torch.exp(-gate) * a * a if c["act"] == "sigmoid" else 1 / torch.cosh(gate) ** 2 if c["act"] == "tanh" \
+        else torch.ones_like(gate)
+    reps = torch.full((gate.shape[0],), c["gate"], device=gate.device)
+    reps[-1] = c["T"] - c["gate"] * (gate.shape[0] - 1)
+    return a.repeat_interleave(reps, 0), p.repeat_interleave(reps, 0), reps
+
+
+def _exact_norm(c, f):
+    d, out = c["d"], f["x"]
+    if c["branch"] != "none":
+        y = f["y"]
+        if y is None:
+            y = torch.zeros_like(out)
+            for j in range(f["slot_row"].shape[1]):
+                row = f["slot_row"][:, j].long()
+                y += torch.where(row >= 0, f["topk_w"][:, j], 0.0)[:, None] * f["y_perm"][row.clamp(min=0)]
+        if f["post_gain"] is not None:
+            y = y / torch.sqrt(y.square().sum(1, keepdim=True) / d + EPS) * f["post_gain"]
+        if f["gate"] is not None:
+            y = y * _exact_gate(c, f["gate"])[0]
+        out = f["rs"] * out + f["bs"] * y
+    h = None
+    if f["next_gain"] is not None:
+        h = out / torch.sqrt(out.square().sum(1, keepdim=True) / d + EPS) * f["next_gain"]
+    return {"out": out if c["branch"] != "none" else None, "h": h}
+
+
+def _exact_norm_bwd(c, f):
+    """Each norm's Jacobian applied to the gradient above it: J = (diag(1) - v v^T / (d q^2)) / q, q = sqrt(mean + eps)."""
+    d = c["d"]
+
+    def back(v, up):
+        q = torch.sqrt(v.square().sum(1, keepdim=True) / d + EPS)
+        return up / q - v * ((v * up).sum(1, keepdim=True) / (d * q ** 3)), v / q
+
+    r = {"dx": None, "dy": None, "d_post_gain": None, "dgate": None, "d_next_gain": None}
+    D = f["d_out"]
+    if f["dh"] is not None:
+        more, unit = back(f["out"], f["dh"] * f["next_gain"])
+        r["d_next_gain"] = (f["dh"] * unit).sum(0)
+        D = D + more
+    r["dx"] = f["rs"] * D
+    if f["y"] is None:
+        return r
+    up = f["bs"] * D
+    gain = f["post_gain"] if f["post_gain"] is not None else torch.ones(d, dtype=torch.float64, device=D.device)
+    unit = back(f["y"], up)[1] if f["post_gain"] is not None else f["y"]
+    if f["gate"] is not None:
+        a, p, reps = _exact_gate(c, f["gate"])
+        each = up * p * unit * gain
+        ends = reps.cumsum(0)
+        if c["gate"] == 1:
+            r["dgate"] = each
+        else:
+            r["dgate"] = torch.stack([each[e - n:e].sum(0) for e, n in zip(ends.tolist(), reps.tolist())])
+        up = up * a
+    if f["post_gain"] is not None:
+        r["d_post_gain"] = (up * unit).sum(0)
+        up = back(f["y"], up * gain)[0]
+    r["dy"] = up
+    return r
+
+
+def _exact_quant(c, f):
+    w, out = f["w"], torch.empty_like(f["w"])
+    for c0 in range(0, c["C"], c["group"]):
+        part = w[..., c0:c0 + c["group"]]
+        # the scale is held in bf16 and stands for itself: the largest magnitude / 7, rounded once to float32 on the way
+        s = (part.abs().amax(-1, keepdim=True).float() / 7).to(torch.bfloat16).double()
+        q = torch.clamp(torch.round(part / torch.where(s > 0, s, 1.0)), -8, 7)
+        out[..., c0:c0 + c["group"]] = q * s
+    return {"w": out}
+
+
+def _exact_w4(c, q, s, C):
+    w = torch.empty(q.shape[0], C, dtype=torch.float64, device=q.device)
+    w[:, 0::2] = (q % 16).double()
+    w[:, 1::2] = (q // 16).double()
+    return (w - 8) * s.double()[:, torch.arange(C, device=q.device) // c["group"]]
+
+
+def _exact_matvec(c, f):
+    return {"y": f["x"] @ _exact_w4(c, f["q"][0], f["s"][0], c["C"]).t()}
+
+
+def _exact_ffn(c, f):
+    y = torch.zeros(c["T"] * c["k"], c["d"], dtype=torch.float64, device=f["x"].device)
+    off = f["offsets"].tolist()
+    for e in range(c["E"]):
+        if off[e] == off[e + 1]:
+            continue
+        x = f["x"][f["row_token"][off[e]:off[e + 1]].long()]
+        g = x @ _exact_w4(c, f["gate"][0][e], f["gate"][1][e], c["d"]).t()
+        u = x @ _exact_w4(c, f["up"][0][e], f["up"][1][e], c["d"]).t()
+        y[off[e]:off[e + 1]] = (g / (1 + torch.exp(-g)) * u) @ _exact_w4(c, f["down"][0][e], f["down"][1][e], c["F"]).t()
+    return {"y": y}
