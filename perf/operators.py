@@ -197,9 +197,9 @@ def prepare(case, seed):
             v["call"] = B.W4Quantize(v["w"], group=case["group"])
             v["values"] = torch.empty_like(v["w"])
         elif op == "matvec":
-            v["call"] = B.W4Matvec(v["x"], B.w4_pack(v["q"], v["s"], group=case["group"]))
+            v["call"] = B.W4Matvec(v["x"], B.moe_w4_pack(v["q"], v["s"], group=case["group"]))
         else:
-            w = [B.w4_pack(*v[name], group=case["group"]) for name in ("gate", "up", "down")]
+            w = [B.moe_w4_pack(*v[name], group=case["group"]) for name in ("gate", "up", "down")]
             v["call"] = B.W4GroupedFfn(v["x"], v["offsets"], *w, a_rows=v["row_token"])
     return v
 
