@@ -130,10 +130,7 @@ def _norm_inputs(c, g):
     if c["op"] == "norm_bwd":
         v["d_out"] = rnd(T, d, std=0.02).to(dt)
         v["dh"] = rnd(T, d, std=0.02).to(dt) if c["next"] else None
-        if c["branch"] != "none":
-            v["out"] = v.pop("x")  # the backward takes the forward's sum; x itself is not needed
-        else:
-            v["out"] = v.pop("x")
+        v["out"] = v.pop("x")  # the backward takes the forward's sum
     return v
 
 
