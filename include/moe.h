@@ -382,6 +382,136 @@ moe_status moe_newton_schulz(int64_t n, int64_t R, int64_t C, moe_dtype dtype, i
                              float a, float b, float c, float eps, const void* g, void* x,
                              void* ws, size_t* ws_bytes, void* stream);
 
+/*
+ * The norms around a block, with its gate and residual scale.  The pages place the
+ * routed layer inside a transformer block ("Training a 1T-Parameter MoE on EU public
+ * infrastructure with PyTorch and TorchTitan", model-configuration table: 74 layers)
+ * and print no norm; root-mean-square norms with a gain are a reading.
+ */
+typedef enum moe_gate_act { MOE_GATE_NONE = 0, MOE_GATE_SIGMOID = 1, MOE_GATE_TANH = 2 } moe_gate_act;
+
+/*
+ * moe_block_norm: what lies between one block's last product and the next block's
+ * first one, in one pass over the rows.
+ *   N(v; g) = g * v / sqrt(mean(v^2) + eps)
+ *   n[t]    = N(y[t]; post_gain), or y[t] when post_gain is NULL
+ *   out[t]  = res_scale * x[t] + branch_scale * a(gate[t / gate_rows]) * n[t]
+ *   h[t]    = N(out[t]; next_gain)
+ *   x       [T,d]    dtype     residual stream
+ *   y       [T,d]    dtype     the block's output, or NULL
+ *   y_perm  [n_rows,d], slot_row [T,k], topk_w [T,k]: the block's output as moe_combine
+ *                              takes it, y[t] = sum_j topk_w[t,j] y_perm[slot_row[t,j]]
+ *                              (float32, not rounded on the way; a slot_row outside
+ *                              [0, n_rows) is skipped), instead of y; else NULL and k,
+ *                              n_rows 0
+ *   post_gain [d]    float32   gain of the norm after the block, or NULL
+ *   gate    [ceil(T/gate_rows),d] dtype   or NULL (gate_rows 0): one row for gate_rows
+ *                              consecutive tokens; 1 = a row a token, >= T = one row
+ *   gate_act                   a: identity, sigmoid or tanh
+ *   next_gain [d]    float32   gain of the norm before the next block, or NULL
+ *   out     [T,d]    dtype     out; may be x itself (same address), no other overlap
+ *   h       [T,d]    dtype     out; given exactly when next_gain is.  Normalises the
+ *                              float32 sum, not its rounding
+ *   y_out   [T,d]    dtype     out: the combined y for the backward (with y_perm), or NULL
+ * Without y and y_perm only h = N(x; next_gain) is computed; post_gain, gate, out and
+ * y_out are then NULL.  A row of a gate group past T is not needed.
+ * Errors: MOE_ERR_INVALID_ARG for combinations other than these, eps < 0 or NaN;
+ * MOE_ERR_UNSUPPORTED for d not a multiple of 64 or above 16,384, T or T*k >= 2^31.
+ */
+moe_status moe_block_norm(int64_t T, int64_t d, int64_t k, moe_dtype dtype, const void* x, const void* y,
+                          const void* y_perm, int64_t n_rows, const int32_t* slot_row, const float* topk_w,
+                          const float* post_gain, const void* gate, int64_t gate_rows, moe_gate_act gate_act,
+                          float res_scale, float branch_scale, float eps, const float* next_gain,
+                          void* out, void* h, void* y_out, void* stream);
+
+/*
+ * moe_block_norm_backward: gradients of moe_block_norm.  Nothing but y and out is kept
+ * from the forward; both norms' statistics are taken again from them.
+ *   D  = d_out + (gradient of h with respect to out)        dx = res_scale * D
+ *   dn = branch_scale * a(gate) * D                         dy = gradient through N(y; post_gain)
+ *   y       [T,d]    dtype     the forward's y (or y_out), or NULL: no branch
+ *   post_gain, gate, gate_rows, gate_act, res_scale, branch_scale, eps: as in the forward
+ *   out     [T,d]    dtype     the forward's out (without a branch: its x)
+ *   next_gain [d]    float32   as in the forward
+ *   d_out   [T,d]    dtype     gradient of out from elsewhere, or NULL (none)
+ *   dh      [T,d]    dtype     gradient of h; out, next_gain, dh and d_next_gain are
+ *                              given together or not at all; d_out or dh must be given
+ *   dx      [T,d]    dtype     out; may be d_out itself (same address), no other overlap
+ *   dy      [T,d]    dtype     out, given exactly when y is
+ *   d_post_gain [d]  float32   out, given exactly when post_gain is
+ *   dgate                      out, given exactly when gate is: [T,d] dtype for
+ *                              gate_rows 1, otherwise float32 sums [ceil(T/gate_rows),d]
+ *   d_next_gain [d]  float32   out
+ *   ws: query with ws == NULL; depends on T, d, gate_rows and on which of post_gain, gate
+ *       and next_gain are NULL
+ * Sums over tokens are float32 and added in a fixed order.  Errors as moe_block_norm.
+ */
+moe_status moe_block_norm_backward(int64_t T, int64_t d, moe_dtype dtype, const void* y, const float* post_gain,
+                                   const void* gate, int64_t gate_rows, moe_gate_act gate_act, float res_scale,
+                                   float branch_scale, float eps, const void* out, const float* next_gain,
+                                   const void* d_out, const void* dh, void* dx, void* dy, float* d_post_gain,
+                                   void* dgate, float* d_next_gain, void* ws, size_t* ws_bytes, void* stream);
+
+/*
+ * 4-bit weights with group scales: a matrix W [R,C] (C a multiple of 32) is held as
+ *   W[r,c] = s[r, c/group] * (q[r,c] - 8),  q in 0..15,  s in bf16,  group 32, 64 or 128
+ * (the last group of a row may be short).  codes and scales are laid out once, in
+ * tiles, by moe_w4_quantize or moe_w4_pack; both buffers are 16-byte aligned and of
+ * these sizes for one matrix, n matrices following one another:
+ */
+#define MOE_W4_TILES(R, C) ((((size_t)(R) + 15) / 16) * (((size_t)(C) + 127) / 128))
+#define MOE_W4_CODES_BYTES(R, C) (MOE_W4_TILES(R, C) * 1024)
+#define MOE_W4_SCALES_BYTES(R, C, group) (MOE_W4_TILES(R, C) * (32 * (128 / (size_t)(group))))
+
+/*
+ * moe_w4_quantize: 4-bit codes and scales of n matrices w [n,R,C] in dtype:
+ *   s = bf16(max over the group of |w| / 7),  q = 8 + round(w / s) clamped to 0..15
+ * (halves to even; a group whose s is 0 has q = 8).
+ * moe_w4_pack: the same layout from codes and scales that are already there:
+ *   q [n,R,C/2] bytes (even column in the low four bits), s [n,R,ceil(C/group)] bf16.
+ * moe_w4_dequantize: w [n,R,C] in dtype = s * (q - 8), rounded once.
+ * Errors: MOE_ERR_INVALID_ARG for sizes <= 0 and null or misaligned pointers;
+ * MOE_ERR_UNSUPPORTED for another group, C not a multiple of 32, R or C above 2^20 or
+ * more than 2^25 tiles.  NaN and infinities in w or s are outside the contract.
+ */
+moe_status moe_w4_quantize(int64_t n, int64_t R, int64_t C, moe_dtype dtype, int64_t group, const void* w,
+                           void* codes, void* scales, void* stream);
+moe_status moe_w4_pack(int64_t n, int64_t R, int64_t C, int64_t group, const void* q, const void* s, void* codes,
+                       void* scales, void* stream);
+moe_status moe_w4_dequantize(int64_t n, int64_t R, int64_t C, moe_dtype dtype, int64_t group, const void* codes,
+                             const void* scales, void* w, void* stream);
+
+/*
+ * moe_w4_matvec: y [T,R] = x [T,C] W^T for one 4-bit matrix and few tokens (each
+ * weight is read once for every 16 tokens).  x and y in dtype; products and sums are
+ * float32 (float32 x enters with all its bits).  |x| of 1e34 and above, infinities and
+ * NaN make their own token's y NaN; other tokens are not touched.
+ *   ws: query with ws == NULL (float32 x: 6 T C bytes, else 0)
+ * Errors as moe_w4_pack; MOE_ERR_UNSUPPORTED also for T above 2^19 and for more than
+ * 2^24 pairs of 16 rows of x and 16 rows of W (and float32 x of 2^33 elements).
+ */
+moe_status moe_w4_matvec(int64_t T, int64_t C, int64_t R, moe_dtype dtype, int64_t group, const void* x,
+                         const void* codes, const void* scales, void* y, void* ws, size_t* ws_bytes, void* stream);
+
+/*
+ * moe_w4_grouped_ffn: moe_grouped_ffn over 4-bit experts, for the few rows an expert
+ * has when single tokens are served ("each token uses a few experts": the time is then
+ * the bytes of the experts that are used).  Arguments as moe_grouped_ffn, with codes and
+ * scales of W_g and W_u (E matrices [F,d]) and W_d (E matrices [d,F]) in one group size.
+ * The hidden activations between the two products are held in 16 significant bits
+ * (bf16 layers) or 24 (float32 layers).  Rows offsets[E].. of y_perm are left as they
+ * were.  Any number of rows is computed; from some hundred rows an expert on
+ * moe_w4_dequantize followed by moe_grouped_ffn is faster.
+ *   ws: query with ws == NULL (4 n_max F bytes; float32: 6 (n_max F + rows of x_in * d))
+ * Errors as moe_grouped_ffn and moe_w4_pack; MOE_ERR_UNSUPPORTED also for n_max above
+ * 2^19 and as moe_w4_matvec for n_max + 16 E rows (x_in may hold 2^32 bytes and more).
+ */
+moe_status moe_w4_grouped_ffn(int64_t n_max, int64_t d, int64_t E, int64_t F, moe_dtype dtype, int64_t group,
+                              const void* x_in, int64_t n_in, const int32_t* a_rows, const int32_t* offsets,
+                              const void* gate_codes, const void* gate_scales, const void* up_codes,
+                              const void* up_scales, const void* down_codes, const void* down_scales,
+                              void* y_perm, void* ws, size_t* ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

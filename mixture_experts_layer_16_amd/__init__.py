@@ -6,4 +6,6 @@ include/moe.h); `binding` marshals torch device tensors into it and
 """
 from . import binding, workloads  # noqa: F401
 from .binding import (moe_combine, moe_grouped_ffn, moe_layer_forward, moe_permute,  # noqa: F401
-                      moe_route, LayerForward, MoEError)
+                      moe_route, moe_block_norm, moe_block_norm_backward,
+                      moe_w4_grouped_ffn, moe_w4_matvec, moe_w4_pack, moe_w4_quantize, BlockNorm, BlockNormBackward,
+                      LayerForward, MoEError, W4GroupedFfn, W4Matvec, W4Quantize, W4Weights)

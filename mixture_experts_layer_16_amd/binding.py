@@ -8,6 +8,7 @@ no fallback of any kind, and a missing library is an error.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -21,7 +22,8 @@ MOE_F32, MOE_BF16 = 0, 1
 STATUS = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED", 3: "MOE_ERR_WORKSPACE", 4: "MOE_ERR_HIP"}
 EXPORTS = ("moe_route", "moe_permute", "moe_grouped_ffn", "moe_combine", "moe_layer_forward", "moe_newton_schulz",
            "moe_grouped_ffn_backward", "moe_combine_backward", "moe_route_backward", "moe_layer_backward",
-           "moe_layer_forward_noalloc")
+           "moe_layer_forward_noalloc", "moe_block_norm", "moe_block_norm_backward", "moe_w4_quantize", "moe_w4_pack",
+           "moe_w4_dequantize", "moe_w4_matvec", "moe_w4_grouped_ffn")
 
 
 class MoEError(RuntimeError):
@@ -51,7 +53,19 @@ _SIGS = {
                            _szp, _vp],
     "moe_layer_backward": [_i64, _i64, _i64, _i64, _i64, _int, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                            _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _szp, _vp],
+    "moe_block_norm": [_i64, _i64, _i64, _int, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _int, _f32, _f32, _f32,
+                       _vp, _vp, _vp, _vp, _vp],
+    "moe_block_norm_backward": [_i64, _i64, _int, _vp, _vp, _vp, _i64, _int, _f32, _f32, _f32, _vp, _vp, _vp, _vp,
+                                _vp, _vp, _vp, _vp, _vp, _vp, _szp, _vp],
+    "moe_w4_quantize": [_i64, _i64, _i64, _int, _i64, _vp, _vp, _vp, _vp],
+    "moe_w4_pack": [_i64, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp],
+    "moe_w4_dequantize": [_i64, _i64, _i64, _int, _i64, _vp, _vp, _vp, _vp],
+    "moe_w4_matvec": [_i64, _i64, _i64, _int, _i64, _vp, _vp, _vp, _vp, _vp, _szp, _vp],
+    "moe_w4_grouped_ffn": [_i64, _i64, _i64, _i64, _int, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                           _vp, _vp, _szp, _vp],
 }
+
+GATE_ACTS = {"none": 0, "sigmoid": 1, "tanh": 2}
 
 MUON_COEFFS = (3.4445, -4.7750, 2.0315)
 
@@ -357,3 +371,275 @@ def moe_layer_forward(x, w_router, bias, w_gate, w_up, w_down, k: int, topk_ids=
                      want_offsets, want_y_perm, want_gu)
     L()
     return L
+
+
+def _on(dev: torch.device):
+    """Makes dev the current device for a launch if another one is."""
+    return torch.cuda.device(dev) if dev.index != torch.cuda.current_device() else contextlib.nullcontext()
+
+
+def _same(name: str, t: Optional[torch.Tensor], dev, dtype, shape):
+    """Checks one operand: where it is given, it has this device, type and shape and is dense."""
+    if t is None:
+        return
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _gate_args(gate, gate_rows: int, gate_act: str, T: int, d: int, dev, dtype):
+    if gate_act not in GATE_ACTS:
+        raise ValueError(f"gate_act must be one of {sorted(GATE_ACTS)}")
+    if gate is None:
+        return 0, 0, GATE_ACTS[gate_act]
+    if gate_rows < 1:
+        raise ValueError("gate_rows must be at least 1")
+    groups = -(-T // gate_rows)
+    _same("gate", gate, dev, dtype, (groups, d))
+    return groups, gate_rows, GATE_ACTS[gate_act]
+
+
+class BlockNorm:
+    """moe_block_norm with its outputs allocated once.  The block's output is y, or
+    (y_perm, slot_row, topk_w) as moe_combine takes it, or nothing (the norm before a
+    first block).  Calling it fills and returns the object: out, h and y_out are None
+    where they are not computed.  out=x writes the new residual stream over x."""
+
+    def __init__(self, x, y=None, y_perm=None, slot_row=None, topk_w=None, post_gain=None, gate=None,
+                 gate_rows: int = 0, gate_act: str = "none", next_gain=None, res_scale: float = 1.0,
+                 branch_scale: float = 1.0, eps: float = 1e-6, out=None, want_y: bool = False):
+        T, d = x.shape
+        dev, dt = x.device, x.dtype
+        k = n_rows = 0
+        _same("x", x, dev, dt, (T, d))
+        _same("y", y, dev, dt, (T, d))
+        if y_perm is not None:
+            if slot_row is None or topk_w is None or slot_row.dim() != 2:
+                raise ValueError("y_perm needs slot_row [T, k] and topk_w [T, k]")
+            k, n_rows = slot_row.shape[1], y_perm.shape[0]
+            _same("y_perm", y_perm, dev, dt, (n_rows, d))
+            _same("slot_row", slot_row, dev, torch.int32, (T, k))
+            _same("topk_w", topk_w, dev, torch.float32, (T, k))
+        _same("post_gain", post_gain, dev, torch.float32, (d,))
+        _same("next_gain", next_gain, dev, torch.float32, (d,))
+        _, rows, act = _gate_args(gate, gate_rows, gate_act, T, d, dev, dt)
+        branch = y is not None or y_perm is not None
+        _same("out", out, dev, dt, (T, d))
+        self.out = (torch.empty_like(x) if out is None else out) if branch else out
+        self.h = torch.empty_like(x) if next_gain is not None else None
+        self.y_out = torch.empty_like(x) if want_y else None
+        self.t = (x, y, y_perm, slot_row, topk_w, post_gain, gate, next_gain)
+        self.dev = dev
+        self.args = (T, d, k, dtype_code(dt), _p(x), _p(y), _p(y_perm), n_rows, _p(slot_row), _p(topk_w),
+                     _p(post_gain), _p(gate), rows, act, res_scale, branch_scale, eps, _p(next_gain), _p(self.out),
+                     _p(self.h), _p(self.y_out))
+
+    def __call__(self):
+        with _on(self.dev):
+            _check("moe_block_norm", lib().moe_block_norm(*self.args, _stream(self.dev)))
+        return self
+
+
+def moe_block_norm(x, y=None, **kw):
+    """One call of the norms around a block (arguments as BlockNorm); returns the
+    BlockNorm object holding out, h and y_out."""
+    return BlockNorm(x, y, **kw)()
+
+
+class BlockNormBackward:
+    """moe_block_norm_backward with its outputs and workspace allocated once.  out is the
+    forward's out (its x where there was no branch), y its y or y_out.  dx, dy,
+    d_post_gain, dgate and d_next_gain are None where there is nothing to differentiate;
+    dgate is float32 [groups, d], or [T, d] in the gate's type for gate_rows 1.
+    dx=d_out writes over the incoming gradient."""
+
+    def __init__(self, d_out=None, dh=None, out=None, y=None, post_gain=None, gate=None, gate_rows: int = 0,
+                 gate_act: str = "none", next_gain=None, res_scale: float = 1.0, branch_scale: float = 1.0,
+                 eps: float = 1e-6, dx=None):
+        if next_gain is None:      # out is not read without the norm that follows it
+            out = None
+        if d_out is None and dh is None:
+            raise ValueError("d_out or dh must be given")
+        like = dh if d_out is None else d_out
+        T, d = like.shape
+        dev, dt = like.device, like.dtype
+        for name, t in (("d_out", d_out), ("dh", dh), ("out", out), ("y", y), ("dx", dx)):
+            _same(name, t, dev, dt, (T, d))
+        _same("post_gain", post_gain, dev, torch.float32, (d,))
+        _same("next_gain", next_gain, dev, torch.float32, (d,))
+        groups, rows, act = _gate_args(gate, gate_rows, gate_act, T, d, dev, dt)
+        f32 = dict(dtype=torch.float32, device=dev)
+        self.dx = torch.empty_like(like) if dx is None else dx
+        self.dy = torch.empty_like(like) if y is not None else None
+        self.d_post_gain = torch.empty(d, **f32) if post_gain is not None else None
+        self.dgate = None if gate is None else torch.empty_like(gate) if rows == 1 else torch.empty(groups, d, **f32)
+        self.d_next_gain = torch.empty(d, **f32) if next_gain is not None else None
+        self.t = (d_out, dh, out, y, post_gain, gate, next_gain)
+        self.dev = dev
+        self.args = (T, d, dtype_code(dt), _p(y), _p(post_gain), _p(gate), rows, act, res_scale, branch_scale, eps,
+                     _p(out), _p(next_gain), _p(d_out), _p(dh), _p(self.dx), _p(self.dy), _p(self.d_post_gain),
+                     _p(self.dgate), _p(self.d_next_gain))
+        need = _query("moe_block_norm_backward", *self.args)
+        self.ws = _ws(need, dev)
+        self._n = ctypes.c_size_t(self.ws.numel())
+        self._ws_p = _p(self.ws)
+
+    def __call__(self):
+        with _on(self.dev):
+            _check("moe_block_norm_backward",
+                   lib().moe_block_norm_backward(*self.args, self._ws_p, ctypes.byref(self._n), _stream(self.dev)))
+        return self
+
+
+def moe_block_norm_backward(d_out=None, dh=None, **kw):
+    """One call of the block norm's backward (arguments as BlockNormBackward); returns the
+    object holding dx, dy, d_post_gain, dgate and d_next_gain."""
+    return BlockNormBackward(d_out, dh, **kw)()
+
+
+class W4Weights:
+    """n matrices [R, C] of 4-bit weights with one scale for `group` columns of a row, in
+    the library's layout (made by moe_w4_quantize or moe_w4_pack)."""
+
+    def __init__(self, n: int, R: int, C: int, group: int, dev):
+        if group not in (32, 64, 128):
+            raise MoEError("4-bit weights", 2)
+        self.n, self.R, self.C, self.group = n, R, C, group
+        tiles = n * (-(-R // 16)) * (-(-C // 128))
+        self.codes = torch.empty(tiles * 1024, dtype=torch.uint8, device=dev)
+        self.scales = torch.empty(tiles * 16 * (128 // group), dtype=torch.bfloat16, device=dev)
+
+    @property
+    def device(self):
+        return self.codes.device
+
+    def dequantize(self, dtype=torch.bfloat16, out=None):
+        """The values [n, R, C] that the codes and scales stand for, rounded once to dtype."""
+        dev = self.device
+        if out is None:
+            out = torch.empty(self.n, self.R, self.C, dtype=dtype, device=dev)
+        _same("out", out, dev, out.dtype, (self.n, self.R, self.C))
+        with _on(dev):
+            _check("moe_w4_dequantize",
+                   lib().moe_w4_dequantize(self.n, self.R, self.C, dtype_code(out.dtype), self.group, _p(self.codes),
+                                           _p(self.scales), _p(out), _stream(dev)))
+        return out
+
+
+class W4Quantize:
+    """moe_w4_quantize of w [R, C] or [n, R, C] with its W4Weights allocated once."""
+
+    def __init__(self, w, group: int = 128):
+        self.w = w if w.dim() == 3 else w.unsqueeze(0)
+        n, R, C = self.w.shape
+        self.out = W4Weights(n, R, C, group, w.device)
+        self.args = (n, R, C, dtype_code(w.dtype), group, _p(self.w), _p(self.out.codes), _p(self.out.scales))
+
+    def __call__(self) -> W4Weights:
+        dev = self.w.device
+        with _on(dev):
+            _check("moe_w4_quantize", lib().moe_w4_quantize(*self.args, _stream(dev)))
+        return self.out
+
+
+def moe_w4_quantize(w, group: int = 128) -> W4Weights:
+    """4-bit codes and scales of w [R, C] or [n, R, C]."""
+    return W4Quantize(w, group)()
+
+
+def moe_w4_pack(q, s, group: int = 128) -> W4Weights:
+    """W4Weights from codes q [n, R, C/2] (uint8, the even column in the low half) and
+    scales s [n, R, ceil(C/group)] (bf16)."""
+    n, R, half = q.shape
+    dev = q.device
+    out = W4Weights(n, R, 2 * half, group, dev)
+    _same("q", q, dev, torch.uint8, (n, R, half))
+    _same("s", s, dev, torch.bfloat16, (n, R, -(-2 * half // group)))
+    with _on(dev):
+        _check("moe_w4_pack", lib().moe_w4_pack(n, R, 2 * half, group, _p(q), _p(s), _p(out.codes), _p(out.scales),
+                                                _stream(dev)))
+    return out
+
+
+class W4Matvec:
+    """moe_w4_matvec: y [T, R] = x [T, C] W^T with its output and workspace allocated once."""
+
+    def __init__(self, x, w: W4Weights, out=None):
+        T = x.shape[0]
+        if w.n != 1:
+            raise ValueError("moe_w4_matvec takes one matrix")
+        dev = x.device
+        _same("x", x, dev, x.dtype, (T, w.C))
+        _same("weights", w.codes, dev, torch.uint8, w.codes.shape)
+        _same("out", out, dev, x.dtype, (T, w.R))
+        self.y = torch.empty(T, w.R, dtype=x.dtype, device=dev) if out is None else out
+        self.t = (x, w)
+        self.dev = dev
+        self.args = (T, w.C, w.R, dtype_code(x.dtype), w.group, _p(x), _p(w.codes), _p(w.scales), _p(self.y))
+        self.ws = _ws(_query("moe_w4_matvec", *self.args), dev)
+        self._n = ctypes.c_size_t(self.ws.numel())
+        self._ws_p = _p(self.ws)
+
+    def __call__(self):
+        with _on(self.dev):
+            _check("moe_w4_matvec", lib().moe_w4_matvec(*self.args, self._ws_p, ctypes.byref(self._n),
+                                                        _stream(self.dev)))
+        return self.y
+
+
+def moe_w4_matvec(x, w: W4Weights, out=None):
+    """y [T, R] = x [T, C] W^T over one 4-bit matrix."""
+    return W4Matvec(x, w, out)()
+
+
+class W4GroupedFfn:
+    """moe_w4_grouped_ffn with its output and workspace allocated once: the SwiGLU FFN of
+    each expert over its rows, on 4-bit weights gate and up (E matrices [F, d]) and down
+    (E matrices [d, F]).  x_in, offsets, a_rows, n_max and y_perm as moe_grouped_ffn."""
+
+    def __init__(self, x_in, offsets, gate: W4Weights, up: W4Weights, down: W4Weights, a_rows=None, n_max=None,
+                 y_perm=None):
+        E, F, d, group = gate.n, gate.R, gate.C, gate.group
+        dev, dt = x_in.device, x_in.dtype
+        for name, w, shape in (("up", up, (E, F, d, group)), ("down", down, (E, d, F, group))):
+            if (w.n, w.R, w.C, w.group) != shape:
+                raise ValueError(f"{name} is {(w.n, w.R, w.C)} in groups of {w.group}, expected {shape}")
+        for name, w in (("gate", gate), ("up", up), ("down", down)):
+            _same(name, w.codes, dev, torch.uint8, w.codes.shape)
+        _same("x_in", x_in, dev, dt, (x_in.shape[0], d))
+        _same("offsets", offsets, dev, torch.int32, (E + 1,))
+        if a_rows is None:
+            if n_max is not None and n_max > x_in.shape[0]:
+                raise ValueError("n_max is larger than x_in")
+            n_max, n_in = x_in.shape[0] if n_max is None else n_max, 0
+        else:
+            n_max, n_in = (a_rows.numel() if n_max is None else n_max), x_in.shape[0]
+            _same("a_rows", a_rows, dev, torch.int32, a_rows.shape)
+            if a_rows.numel() < n_max:
+                raise ValueError("a_rows has fewer than n_max entries")
+        _same("y_perm", y_perm, dev, dt, (n_max, d))
+        self.y_perm = torch.empty(n_max, d, dtype=dt, device=dev) if y_perm is None else y_perm
+        self.t = (x_in, offsets, gate, up, down, a_rows)
+        self.dev = dev
+        self.args = (n_max, d, E, F, dtype_code(dt), group, _p(x_in), n_in, _p(a_rows), _p(offsets), _p(gate.codes),
+                     _p(gate.scales), _p(up.codes), _p(up.scales), _p(down.codes), _p(down.scales), _p(self.y_perm))
+        self.ws = _ws(_query("moe_w4_grouped_ffn", *self.args), dev)
+        self._n = ctypes.c_size_t(self.ws.numel())
+        self._ws_p = _p(self.ws)
+
+    def __call__(self):
+        with _on(self.dev):
+            _check("moe_w4_grouped_ffn", lib().moe_w4_grouped_ffn(*self.args, self._ws_p, ctypes.byref(self._n),
+                                                                  _stream(self.dev)))
+        return self.y_perm
+
+
+def moe_w4_grouped_ffn(x_in, offsets, gate: W4Weights, up: W4Weights, down: W4Weights, a_rows=None, n_max=None,
+                       y_perm=None):
+    """y_perm [n_max, d]: the SwiGLU FFN of each 4-bit expert over its rows."""
+    return W4GroupedFfn(x_in, offsets, gate, up, down, a_rows, n_max, y_perm)()

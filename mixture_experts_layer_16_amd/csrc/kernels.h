@@ -104,4 +104,67 @@ hipError_t launch_route_backward(int dtype, int64_t T, int64_t d, int64_t E, int
 hipError_t launch_unpermute(int dtype, int64_t T, int64_t d, int64_t k, const void* dx_perm,
                             const int32_t* slot_row, void* dx, hipStream_t stream);
 
+// The norms around a block (block_norm.hip).  Pointers are nullptr where a part is absent.
+struct BlockNormArgs {
+  int64_t T;
+  int d, k, n_rows;
+  const void *x, *y, *y_perm;        // I/O type; y or (y_perm, slot_row, topk_w) when has_y
+  const int32_t* slot_row;
+  const float* topk_w;
+  bool has_y;
+  const float *post_gain, *next_gain;
+  const void* gate;                  // [ceil(T / gate_rows), d]
+  int64_t gate_rows;
+  int gate_act;
+  float res_scale, branch_scale, eps;
+  void *out, *h, *y_out;
+};
+hipError_t launch_block_norm(int dtype, const BlockNormArgs& a, int num_cu, hipStream_t stream);
+
+// How the backward deals rows to teams: `rows` consecutive rows each; with
+// teams_per_group > 0 each gate group has that many teams of its own, otherwise a
+// team's rows cover whole groups.
+struct RowPlan {
+  int teams;
+  int teams_per_group;
+  int64_t rows;
+};
+RowPlan block_norm_row_plan(int64_t T, int64_t d, int64_t gate_rows);
+struct BlockNormBackwardArgs {
+  int64_t T;
+  int d;
+  const void *y, *gate, *out, *d_out, *dh;
+  const float *post_gain, *next_gain;
+  int64_t gate_rows;
+  int gate_act;
+  float res_scale, branch_scale, eps;
+  void *dx, *dy, *dgate;
+  float *d_post_gain, *d_next_gain;
+  float *part_post, *part_next, *part_gate;   // [teams, d] each
+  RowPlan plan;
+};
+hipError_t launch_block_norm_backward(int dtype, const BlockNormBackwardArgs& a, hipStream_t stream);
+
+// 4-bit weights (w4.h): n matrices [R, C], groups of 32, 64 or 128 columns.
+hipError_t launch_w4_quantize(int dtype, int64_t n, int64_t R, int64_t C, int group, const void* w, void* codes,
+                              void* scales, hipStream_t stream);
+hipError_t launch_w4_pack(int64_t n, int64_t R, int64_t C, int group, const void* q, const void* s, void* codes,
+                          void* scales, hipStream_t stream);
+hipError_t launch_w4_dequantize(int dtype, int64_t n, int64_t R, int64_t C, int group, const void* codes,
+                                const void* scales, void* w, hipStream_t stream);
+
+// y [T, R] = x [T, C] W^T.  x_planes: 3 T C bf16 of scratch for float32 x, else unused.
+hipError_t launch_w4_matvec(int dtype, int64_t T, int64_t C, int64_t R, int group, const void* x, const void* codes,
+                            const void* scales, void* y, void* x_planes, hipStream_t stream);
+
+// The grouped SwiGLU FFN over 4-bit experts (codes and scales: gate, up, down).
+// x_planes: 3 n_in d bf16 (float32 x only); h_planes: n_max F bf16, twice for bf16
+// layers, three times for float32 ones.
+hipError_t launch_w4_grouped_ffn(int dtype, int64_t n_max, int64_t d, int64_t E, int64_t F, int group, const void* x,
+                                 int64_t n_in, const int32_t* a_rows, const int32_t* offsets, const void* const* codes,
+                                 const void* const* scales, void* y_perm, void* x_planes, void* h_planes,
+                                 hipStream_t stream);
+// Token tiles that a grouped product launches for n_max rows of E experts.
+int64_t w4_token_tiles(int64_t n_max, int64_t E);
+
 }  // namespace moe

@@ -9,6 +9,7 @@
 
 #include "kernels.h"
 #include "moe.h"
+#include "w4.h"
 
 namespace {
 
@@ -145,6 +146,38 @@ void carve_route_backward(Carver& c, moe::RouteBackwardScratch& w, int64_t T, in
   w.split_partial = w.splits > 1 ? static_cast<float*>(c.take((size_t)w.splits * E * d * 4)) : nullptr;
   w.bias_partial = static_cast<float*>(c.take((size_t)w.bias_chunks * E * 4));
 }
+
+constexpr int64_t kMaxNormDim = 16384;
+
+// The checks that the block norm's two directions share.
+moe_status check_block_norm(int64_t T, int64_t d, moe_dtype dtype, const void* gate, int64_t gate_rows,
+                            moe_gate_act gate_act, float eps) {
+  if (T <= 0 || d <= 0 || !(eps >= 0.0f)) return MOE_ERR_INVALID_ARG;
+  if (gate != nullptr ? gate_rows <= 0 : gate_rows != 0) return MOE_ERR_INVALID_ARG;
+  if (gate_act != MOE_GATE_NONE && gate_act != MOE_GATE_SIGMOID && gate_act != MOE_GATE_TANH)
+    return MOE_ERR_INVALID_ARG;
+  if (d % 64 != 0 || d > kMaxNormDim || T >= kIdxLimit) return MOE_ERR_UNSUPPORTED;
+  return check_dtype(dtype);
+}
+
+constexpr int64_t kMaxW4Tiles = int64_t(1) << 25;
+constexpr int64_t kMaxW4Rows = int64_t(1) << 19;
+
+// Sizes of n 4-bit matrices [R, C].
+moe_status check_w4(int64_t n, int64_t R, int64_t C, int64_t group) {
+  if (n <= 0 || R <= 0 || C <= 0) return MOE_ERR_INVALID_ARG;
+  if ((group != 32 && group != 64 && group != 128) || C % 32 != 0 || R > kMaxDim || C > kMaxDim ||
+      n > kMaxW4Tiles || n * (moe::w4_row_tiles(R) * moe::w4_col_tiles(C)) > kMaxW4Tiles)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+// A product's grid: row tiles by token tiles within the launch limits (256 threads each).
+bool w4_grid_fits(int64_t R, int64_t token_tiles) {
+  return token_tiles <= 65535 && moe::w4_row_tiles(R) * token_tiles < (int64_t(1) << 24);
+}
+// The kernel that splits float32 activations takes 1,024 elements a workgroup.
+bool w4_split_fits(int64_t rows, int64_t C) { return rows * C < (int64_t(1) << 33); }
 
 }  // namespace
 
@@ -481,6 +514,155 @@ moe_status moe_layer_forward(int64_t T, int64_t d, int64_t E, int64_t k, int64_t
                                                y_perm, h, gu_out, ncu, s))) != MOE_OK)
     return st;
   return hip_status(moe::launch_combine(dtype, T, d, k, y_perm, slot_row, w, y, s));
+}
+
+moe_status moe_block_norm(int64_t T, int64_t d, int64_t k, moe_dtype dtype, const void* x, const void* y,
+                          const void* y_perm, int64_t n_rows, const int32_t* slot_row, const float* topk_w,
+                          const float* post_gain, const void* gate, int64_t gate_rows, moe_gate_act gate_act,
+                          float res_scale, float branch_scale, float eps, const float* next_gain, void* out,
+                          void* h, void* y_out, void* stream) {
+  moe_status st = check_block_norm(T, d, dtype, gate, gate_rows, gate_act, eps);
+  if (st != MOE_OK) return st;
+  const bool combined = y_perm != nullptr, branch = combined || y != nullptr;
+  if (combined) {
+    if (y != nullptr || k <= 0 || n_rows <= 0 || !ok16(y_perm) || !ok4(slot_row) || !ok4(topk_w))
+      return MOE_ERR_INVALID_ARG;
+    if (k >= kIdxLimit || T * k >= kIdxLimit || n_rows >= kIdxLimit) return MOE_ERR_UNSUPPORTED;
+  } else if (k != 0 || n_rows != 0 || slot_row || topk_w || y_out) {
+    return MOE_ERR_INVALID_ARG;
+  }
+  if (!ok16(x) || !opt16(y) || !opt16(post_gain) || !opt16(gate) || !opt16(next_gain) || !opt16(out) ||
+      !opt16(h) || !opt16(y_out))
+    return MOE_ERR_INVALID_ARG;
+  if ((next_gain == nullptr) != (h == nullptr) || branch != (out != nullptr)) return MOE_ERR_INVALID_ARG;
+  if (!branch && (post_gain || gate || !next_gain)) return MOE_ERR_INVALID_ARG;
+  int ncu = 0;
+  if ((st = num_cu(&ncu)) != MOE_OK) return st;
+  moe::BlockNormArgs a{};
+  a.T = T; a.d = (int)d; a.k = (int)k; a.n_rows = (int)n_rows;
+  a.x = x; a.y = y; a.y_perm = y_perm; a.slot_row = slot_row; a.topk_w = topk_w;
+  a.has_y = branch;
+  a.post_gain = post_gain; a.next_gain = next_gain;
+  a.gate = gate; a.gate_rows = gate_rows; a.gate_act = gate_act;
+  a.res_scale = res_scale; a.branch_scale = branch_scale; a.eps = eps;
+  a.out = out; a.h = h; a.y_out = y_out;
+  return hip_status(moe::launch_block_norm(dtype, a, ncu, static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_block_norm_backward(int64_t T, int64_t d, moe_dtype dtype, const void* y, const float* post_gain,
+                                   const void* gate, int64_t gate_rows, moe_gate_act gate_act, float res_scale,
+                                   float branch_scale, float eps, const void* out, const float* next_gain,
+                                   const void* d_out, const void* dh, void* dx, void* dy, float* d_post_gain,
+                                   void* dgate, float* d_next_gain, void* ws, size_t* ws_bytes, void* stream) {
+  moe_status st = check_block_norm(T, d, dtype, gate, gate_rows, gate_act, eps);
+  if (st != MOE_OK) return st;
+  moe::BlockNormBackwardArgs a{};
+  a.plan = moe::block_norm_row_plan(T, d, gate ? gate_rows : 0);
+  const size_t part = (size_t)a.plan.teams * (size_t)d * 4;
+  Carver c(ws);
+  a.part_post = post_gain ? static_cast<float*>(c.take(part)) : nullptr;
+  a.part_next = next_gain ? static_cast<float*>(c.take(part)) : nullptr;
+  a.part_gate = a.plan.teams_per_group ? static_cast<float*>(c.take(part)) : nullptr;
+  if (ws == nullptr && ws_bytes != nullptr) {
+    *ws_bytes = c.used;
+    return MOE_OK;
+  }
+  if (!opt16(y) || !opt16(post_gain) || !opt16(gate) || !opt16(out) || !opt16(next_gain) || !opt16(d_out) ||
+      !opt16(dh) || !ok16(dx) || !opt16(dy) || !opt16(d_post_gain) || !opt16(dgate) || !opt16(d_next_gain))
+    return MOE_ERR_INVALID_ARG;
+  const bool next = next_gain != nullptr;
+  if (next != (out != nullptr) || next != (dh != nullptr) || next != (d_next_gain != nullptr) || (!next && !d_out))
+    return MOE_ERR_INVALID_ARG;
+  if ((y == nullptr) != (dy == nullptr) || (post_gain == nullptr) != (d_post_gain == nullptr) ||
+      (gate == nullptr) != (dgate == nullptr) || (y == nullptr && (post_gain || gate)))
+    return MOE_ERR_INVALID_ARG;
+  if (workspace_step(ws, ws_bytes, c.used, &st)) return st;
+  a.T = T; a.d = (int)d;
+  a.y = y; a.gate = gate; a.out = out; a.d_out = d_out; a.dh = dh;
+  a.post_gain = post_gain; a.next_gain = next_gain;
+  a.gate_rows = gate_rows; a.gate_act = gate_act;
+  a.res_scale = res_scale; a.branch_scale = branch_scale; a.eps = eps;
+  a.dx = dx; a.dy = dy; a.dgate = dgate; a.d_post_gain = d_post_gain; a.d_next_gain = d_next_gain;
+  return hip_status(moe::launch_block_norm_backward(dtype, a, static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_w4_quantize(int64_t n, int64_t R, int64_t C, moe_dtype dtype, int64_t group, const void* w,
+                           void* codes, void* scales, void* stream) {
+  moe_status st = check_w4(n, R, C, group);
+  if (st != MOE_OK) return st;
+  if ((st = check_dtype(dtype)) != MOE_OK) return st;
+  if (!ok16(w) || !ok16(codes) || !ok16(scales)) return MOE_ERR_INVALID_ARG;
+  return hip_status(moe::launch_w4_quantize(dtype, n, R, C, (int)group, w, codes, scales,
+                                            static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_w4_pack(int64_t n, int64_t R, int64_t C, int64_t group, const void* q, const void* s, void* codes,
+                       void* scales, void* stream) {
+  moe_status st = check_w4(n, R, C, group);
+  if (st != MOE_OK) return st;
+  if (!ok16(q) || !ok16(s) || !ok16(codes) || !ok16(scales)) return MOE_ERR_INVALID_ARG;
+  return hip_status(moe::launch_w4_pack(n, R, C, (int)group, q, s, codes, scales, static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_w4_dequantize(int64_t n, int64_t R, int64_t C, moe_dtype dtype, int64_t group, const void* codes,
+                             const void* scales, void* w, void* stream) {
+  moe_status st = check_w4(n, R, C, group);
+  if (st != MOE_OK) return st;
+  if ((st = check_dtype(dtype)) != MOE_OK) return st;
+  if (!ok16(codes) || !ok16(scales) || !ok16(w)) return MOE_ERR_INVALID_ARG;
+  return hip_status(moe::launch_w4_dequantize(dtype, n, R, C, (int)group, codes, scales, w,
+                                              static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_w4_matvec(int64_t T, int64_t C, int64_t R, moe_dtype dtype, int64_t group, const void* x,
+                         const void* codes, const void* scales, void* y, void* ws, size_t* ws_bytes, void* stream) {
+  moe_status st = check_w4(1, R, C, group);
+  if (st != MOE_OK) return st;
+  if (T <= 0) return MOE_ERR_INVALID_ARG;
+  if ((st = check_dtype(dtype)) != MOE_OK) return st;
+  if (T > kMaxW4Rows || !w4_grid_fits(R, (T + 15) / 16) || (dtype == MOE_F32 && !w4_split_fits(T, C)))
+    return MOE_ERR_UNSUPPORTED;
+  const size_t need = dtype == MOE_F32 ? round_up((size_t)T * (size_t)C * 6) : 0;
+  if (ws == nullptr && ws_bytes != nullptr) {
+    *ws_bytes = need;
+    return MOE_OK;
+  }
+  if (!ok16(x) || !ok16(codes) || !ok16(scales) || !ok16(y)) return MOE_ERR_INVALID_ARG;
+  if (workspace_step(ws, ws_bytes, need, &st)) return st;
+  return hip_status(moe::launch_w4_matvec(dtype, T, C, R, (int)group, x, codes, scales, y, ws,
+                                          static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_w4_grouped_ffn(int64_t n_max, int64_t d, int64_t E, int64_t F, moe_dtype dtype, int64_t group,
+                              const void* x_in, int64_t n_in, const int32_t* a_rows, const int32_t* offsets,
+                              const void* gate_codes, const void* gate_scales, const void* up_codes,
+                              const void* up_scales, const void* down_codes, const void* down_scales, void* y_perm,
+                              void* ws, size_t* ws_bytes, void* stream) {
+  moe_status st = check_ffn_dims(n_max, d, E, F);
+  if (st != MOE_OK) return st;
+  if ((st = check_w4(E, F, d, group)) != MOE_OK || (st = check_w4(E, d, F, group)) != MOE_OK) return st;
+  if ((st = check_dtype(dtype)) != MOE_OK) return st;
+  if (a_rows != nullptr && n_in <= 0) return MOE_ERR_INVALID_ARG;
+  const int64_t tiles = moe::w4_token_tiles(n_max, E), x_rows = a_rows ? n_in : n_max;
+  const bool f32 = dtype == MOE_F32;
+  if (n_max > kMaxW4Rows || x_rows >= kIdxLimit || !w4_grid_fits(F, tiles) || !w4_grid_fits(d, tiles) ||
+      (f32 && !w4_split_fits(x_rows, d)))
+    return MOE_ERR_UNSUPPORTED;
+  Carver c(ws);
+  void* h = c.take((size_t)n_max * (size_t)F * (f32 ? 6 : 4));
+  void* xp = f32 ? c.take((size_t)x_rows * (size_t)d * 6) : nullptr;
+  if (ws == nullptr && ws_bytes != nullptr) {
+    *ws_bytes = c.used;
+    return MOE_OK;
+  }
+  if (!ok16(x_in) || !opt4(a_rows) || !ok4(offsets) || !ok16(gate_codes) || !ok16(gate_scales) ||
+      !ok16(up_codes) || !ok16(up_scales) || !ok16(down_codes) || !ok16(down_scales) || !ok16(y_perm))
+    return MOE_ERR_INVALID_ARG;
+  if (workspace_step(ws, ws_bytes, c.used, &st)) return st;
+  const void* codes[3] = {gate_codes, up_codes, down_codes};
+  const void* scales[3] = {gate_scales, up_scales, down_scales};
+  return hip_status(moe::launch_w4_grouped_ffn(dtype, n_max, d, E, F, (int)group, x_in, x_rows, a_rows, offsets,
+                                               codes, scales, y_perm, xp, h, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"
