@@ -461,7 +461,8 @@ moe_status moe_block_norm_backward(int64_t T, int64_t d, moe_dtype dtype, const 
  */
 #define MOE_W4_TILES(R, C) ((((size_t)(R) + 15) / 16) * (((size_t)(C) + 127) / 128))
 #define MOE_W4_CODES_BYTES(R, C) (MOE_W4_TILES(R, C) * 1024)
-#define MOE_W4_SCALES_BYTES(R, C, group) (MOE_W4_TILES(R, C) * (32 * (128 / (size_t)(group))))
+#define MOE_W4_ROW_SCALES(C, group) (((((size_t)(C) + 127) / 128) * (128 / (size_t)(group)) + 3) / 4 * 4)
+#define MOE_W4_SCALES_BYTES(R, C, group) ((((size_t)(R) + 15) / 16) * 32 * MOE_W4_ROW_SCALES(C, group))
 
 /*
  * moe_w4_quantize: 4-bit codes and scales of n matrices w [n,R,C] in dtype:
@@ -488,7 +489,8 @@ moe_status moe_w4_dequantize(int64_t n, int64_t R, int64_t C, moe_dtype dtype, i
  * NaN make their own token's y NaN; other tokens are not touched.
  *   ws: query with ws == NULL (float32 x: 6 T C bytes, else 0)
  * Errors as moe_w4_pack; MOE_ERR_UNSUPPORTED also for T above 2^19 and for more than
- * 2^24 pairs of 16 rows of x and 16 rows of W (and float32 x of 2^33 elements).
+ * 2^24 pairs of 16 rows of x and 16 rows of W, and for x of 2^31 elements (float32: a
+ * third of that).
  */
 moe_status moe_w4_matvec(int64_t T, int64_t C, int64_t R, moe_dtype dtype, int64_t group, const void* x,
                          const void* codes, const void* scales, void* y, void* ws, size_t* ws_bytes, void* stream);
@@ -504,7 +506,7 @@ moe_status moe_w4_matvec(int64_t T, int64_t C, int64_t R, moe_dtype dtype, int64
  * moe_w4_dequantize followed by moe_grouped_ffn is faster.
  *   ws: query with ws == NULL (4 n_max F bytes; float32: 6 (n_max F + rows of x_in * d))
  * Errors as moe_grouped_ffn and moe_w4_pack; MOE_ERR_UNSUPPORTED also for n_max above
- * 2^19 and as moe_w4_matvec for n_max + 16 E rows (x_in may hold 2^32 bytes and more).
+ * 2^19 and as moe_w4_matvec for n_max + 16 E rows, and for n_max F of 2^30.
  */
 moe_status moe_w4_grouped_ffn(int64_t n_max, int64_t d, int64_t E, int64_t F, moe_dtype dtype, int64_t group,
                               const void* x_in, int64_t n_in, const int32_t* a_rows, const int32_t* offsets,

@@ -155,7 +155,7 @@ hipError_t launch_w4_dequantize(int dtype, int64_t n, int64_t R, int64_t C, int 
 
 // y [T, R] = x [T, C] W^T.  x_planes: 3 T C bf16 of scratch for float32 x, else unused.
 hipError_t launch_w4_matvec(int dtype, int64_t T, int64_t C, int64_t R, int group, const void* x, const void* codes,
-                            const void* scales, void* y, void* x_planes, hipStream_t stream);
+                            const void* scales, void* y, void* x_planes, int num_cu, hipStream_t stream);
 
 // The grouped SwiGLU FFN over 4-bit experts (codes and scales: gate, up, down).
 // x_planes: 3 n_in d bf16 (float32 x only); h_planes: n_max F bf16, twice for bf16
@@ -163,7 +163,7 @@ hipError_t launch_w4_matvec(int dtype, int64_t T, int64_t C, int64_t R, int grou
 hipError_t launch_w4_grouped_ffn(int dtype, int64_t n_max, int64_t d, int64_t E, int64_t F, int group, const void* x,
                                  int64_t n_in, const int32_t* a_rows, const int32_t* offsets, const void* const* codes,
                                  const void* const* scales, void* y_perm, void* x_planes, void* h_planes,
-                                 hipStream_t stream);
+                                 int num_cu, hipStream_t stream);
 // Token tiles that a grouped product launches for n_max rows of E experts.
 int64_t w4_token_tiles(int64_t n_max, int64_t E);
 

@@ -176,8 +176,8 @@ moe_status check_w4(int64_t n, int64_t R, int64_t C, int64_t group) {
 bool w4_grid_fits(int64_t R, int64_t token_tiles) {
   return token_tiles <= 65535 && moe::w4_row_tiles(R) * token_tiles < (int64_t(1) << 24);
 }
-// The kernel that splits float32 activations takes 1,024 elements a workgroup.
-bool w4_split_fits(int64_t rows, int64_t C) { return rows * C < (int64_t(1) << 33); }
+// The bf16 planes of a product's rows are addressed with 32-bit byte offsets.
+bool w4_rows_fit(int64_t rows, int64_t C, int planes) { return rows * C * planes < (int64_t(1) << 31); }
 
 }  // namespace
 
@@ -620,7 +620,8 @@ moe_status moe_w4_matvec(int64_t T, int64_t C, int64_t R, moe_dtype dtype, int64
   if (st != MOE_OK) return st;
   if (T <= 0) return MOE_ERR_INVALID_ARG;
   if ((st = check_dtype(dtype)) != MOE_OK) return st;
-  if (T > kMaxW4Rows || !w4_grid_fits(R, (T + 15) / 16) || (dtype == MOE_F32 && !w4_split_fits(T, C)))
+  if (T > kMaxW4Rows || !w4_grid_fits(R, (T + 15) / 16) ||
+      !w4_rows_fit(T, C, dtype == MOE_F32 ? 3 : 1))
     return MOE_ERR_UNSUPPORTED;
   const size_t need = dtype == MOE_F32 ? round_up((size_t)T * (size_t)C * 6) : 0;
   if (ws == nullptr && ws_bytes != nullptr) {
@@ -629,7 +630,9 @@ moe_status moe_w4_matvec(int64_t T, int64_t C, int64_t R, moe_dtype dtype, int64
   }
   if (!ok16(x) || !ok16(codes) || !ok16(scales) || !ok16(y)) return MOE_ERR_INVALID_ARG;
   if (workspace_step(ws, ws_bytes, need, &st)) return st;
-  return hip_status(moe::launch_w4_matvec(dtype, T, C, R, (int)group, x, codes, scales, y, ws,
+  int ncu = 0;
+  if ((st = num_cu(&ncu)) != MOE_OK) return st;
+  return hip_status(moe::launch_w4_matvec(dtype, T, C, R, (int)group, x, codes, scales, y, ws, ncu,
                                           static_cast<hipStream_t>(stream)));
 }
 
@@ -646,7 +649,7 @@ moe_status moe_w4_grouped_ffn(int64_t n_max, int64_t d, int64_t E, int64_t F, mo
   const int64_t tiles = moe::w4_token_tiles(n_max, E), x_rows = a_rows ? n_in : n_max;
   const bool f32 = dtype == MOE_F32;
   if (n_max > kMaxW4Rows || x_rows >= kIdxLimit || !w4_grid_fits(F, tiles) || !w4_grid_fits(d, tiles) ||
-      (f32 && !w4_split_fits(x_rows, d)))
+      !w4_rows_fit(x_rows, d, f32 ? 3 : 1) || !w4_rows_fit(n_max, F, f32 ? 3 : 2))
     return MOE_ERR_UNSUPPORTED;
   Carver c(ws);
   void* h = c.take((size_t)n_max * (size_t)F * (f32 ? 6 : 4));
@@ -659,10 +662,13 @@ moe_status moe_w4_grouped_ffn(int64_t n_max, int64_t d, int64_t E, int64_t F, mo
       !ok16(up_codes) || !ok16(up_scales) || !ok16(down_codes) || !ok16(down_scales) || !ok16(y_perm))
     return MOE_ERR_INVALID_ARG;
   if (workspace_step(ws, ws_bytes, c.used, &st)) return st;
+  int ncu = 0;
+  if ((st = num_cu(&ncu)) != MOE_OK) return st;
   const void* codes[3] = {gate_codes, up_codes, down_codes};
   const void* scales[3] = {gate_scales, up_scales, down_scales};
   return hip_status(moe::launch_w4_grouped_ffn(dtype, n_max, d, E, F, (int)group, x_in, x_rows, a_rows, offsets,
-                                               codes, scales, y_perm, xp, h, static_cast<hipStream_t>(stream)));
+                                               codes, scales, y_perm, xp, h, ncu,
+                                               static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -9,11 +9,11 @@
 //          row rt*16 + l%16, columns kt*128 + i*32 + (l/16)*8 + 0..7; in a word,
 //          nibble j is column 2j and nibble j + 4 column 2j + 1 (j = 0..3), so
 //          that nibbles j and j + 4 sit 16 bits apart, as a bf16 pair does
-//   scales [RT, KT] tiles of 16 * 128/group bf16, as [4 row quads][128/group][4 rows]:
-//          what one lane of an MFMA result needs is contiguous
+//   scales [RT, 16, NG] bf16: the scales of each row in order, so that a lane loads
+//          those of several column tiles at once
 //
-// with RT = ceil(R/16), KT = ceil(C/128).  Rows and columns past the matrix have
-// code 8 and scale 0.
+// with RT = ceil(R/16), KT = ceil(C/128), NG = KT * 128/group rounded up to 4.  Rows and
+// columns past the matrix have code 8 and scale 0.
 #pragma once
 
 #include <stdint.h>
@@ -26,5 +26,6 @@ constexpr int kW4TileBytes = kW4Rows * kW4Cols / 2;
 
 inline int64_t w4_row_tiles(int64_t R) { return (R + kW4Rows - 1) / kW4Rows; }
 inline int64_t w4_col_tiles(int64_t C) { return (C + kW4Cols - 1) / kW4Cols; }
+inline int w4_row_scales(int64_t C, int64_t group) { return (int)((w4_col_tiles(C) * (kW4Cols / group) + 3) / 4 * 4); }
 
 }  // namespace moe

@@ -2,48 +2,84 @@
 // expert e, plain or as the gate/up pair of a SwiGLU expert.
 //
 // With few rows an expert the time is the weights' bytes.  A wavefront streams tiles
-// of 16 weight rows x 128 columns; the weights are the A operand of 16x16x32 bf16
-// MFMAs and up to 16 token rows the B operand, so one pass over the weights serves
-// 16 rows.  Per code there is then no multiply on the vector unit, only the unpacking:
+// of 16 weight rows x 128 columns; up to 16 token rows are the A operand of 16x16x32 bf16
+// MFMAs and the weights the B operand, so one pass over the weights serves 16 rows, and a
+// lane's results all belong to one weight row: a group's scale is one number a lane.  Per
+// code there is then no multiply on the vector unit, only the unpacking:
 //
-//   a bf16 with exponent 2^p holds p' = 7 fraction bits, so OR-ing a 4-bit code into
-//   its fraction adds the code in steps of 2^(p - 7 + bit): 0x4300 | q = 128 + q and,
-//   with the code three bits higher, 0x4180 | q << 3 = 16 + q.  One shift and one
-//   and-or make two operands (v_and_or_b32).
+//   a bf16 with exponent 2^p holds 7 fraction bits, so OR-ing a 4-bit code into its
+//   fraction adds the code in steps of 2^(p - 7 + bit): 0x4300 | q = 128 + q and, with
+//   the code three bits higher, 0x4180 | q << 3 = 16 + q.  One shift and one and-or make
+//   two operands (v_and_or_b32).
 //
 // The offsets (136 or 24 with the code's own 8) are taken out by the matrix unit too:
-// a group's accumulators start at (-136 | -24) . x, one MFMA with a constant A operand
+// a group's accumulators start at x . (-136 | -24), one MFMA with a constant B operand
 // shared by every tile of the wavefront, instead of at zero.  What is then left per
 // group is total += s * acc, one FMA a result.  All sums are float32.
 //
-// B operands are bf16 planes whose sum is the float32 activation: one plane for bf16
+// A operands are bf16 planes whose sum is the float32 activation: one plane for bf16
 // activations, three for float32 ones (24 bits), two for the hidden activations of a
 // bf16 expert, which so keep 16 bits instead of being rounded to 8 between the two
 // products (the weight stream, not the MFMAs, is what bounds the kernel).
 //
-// The wavefronts of a workgroup split the columns and add their totals in LDS in a
+// The wavefronts that share a tile split its columns and add their totals in LDS in a
 // fixed order; there are no atomics, results are bit-reproducible.
 #include "common.h"
 #include "kernels.h"
 #include "tile_walk.h"
 #include "w4.h"
 
+#ifndef W4_D1
+#define W4_D1 4
+#endif
+#ifndef W4_D2
+#define W4_D2 2
+#endif
+#ifndef W4_KSD
+#define W4_KSD 4
+#endif
+#ifndef W4_KSU
+#define W4_KSU 4
+#endif
+#ifndef W4_NTD
+#define W4_NTD 2
+#endif
+#ifndef W4_NTU
+#define W4_NTU 2
+#endif
+#ifndef W4_DS
+#define W4_DS 4
+#endif
+#ifndef W4_NTM
+#define W4_NTM 2
+#endif
+#ifndef W4_NTMD
+#define W4_NTMD 2
+#endif
+#ifndef W4_SCHED
+#define W4_SCHED __builtin_amdgcn_sched_barrier(0)
+#endif
+#ifndef W4_OCC
+#define W4_OCC 3
+#endif
+#ifndef W4_FULL
+#define W4_FULL 12
+#endif
 namespace moe {
 
 namespace {
 
-constexpr int kWaves = 4;      // wavefronts of a workgroup, each a share of the columns
-constexpr int kDepth = 3;      // column tiles a wavefront has in flight
-constexpr int kTok = 16;       // token rows of a workgroup
+constexpr int kWaves = 4;      // wavefronts of a workgroup
+constexpr int kTok = 16;       // token rows of an MFMA
+constexpr int kStreamed = 2;   // weights pass through the caches without staying (nt)
 
 struct W4Args {
   const bf16* x;               // [planes][n_in, C]
-  int64_t x_plane;             // elements between planes
   int64_t n_in;
   const int32_t* a_rows;       // row r reads x[a_rows[r]], or nullptr
   const int32_t* offsets;      // [E + 1] device, or nullptr: rows 0 .. n_max-1 of one matrix
   int64_t n_max;
-  int E, C, R, KT, RT;
+  int E, C, R, KT, RT, NG;     // NG: scales of a weight row, padded (w4.h)
   const uint32_t* codes[2];
   const uint16_t* scales[2];
   void* y;                     // [n_max, R], or bf16 planes [planes][n_max, R]
@@ -52,59 +88,67 @@ struct W4Args {
 
 struct TokenTile {
   int e;                       // expert, or -1: no such tile
-  int64_t row0;
-  int rows;                    // 1 .. kTok
+  int row0, rows;              // rows: 1 .. tok
 };
 
-// The slot-th tile of kTok rows over the experts' segments (tile_walk.h's bounds: the
-// offsets are not trusted).  Every wavefront scans for itself: 64 experts a step, a
-// running maximum and a running sum over the lanes.
-__device__ __forceinline__ TokenTile find_tile(const int32_t* offsets, int E, int64_t n_max, int slot) {
+// Inclusive scans over the 64 lanes in registers: shifts inside each row of 16 lanes,
+// then the rows' last values passed on.
+template <typename F> __device__ __forceinline__ int lane_scan(int v, int identity, F f) {
+  v = f(v, __builtin_amdgcn_update_dpp(identity, v, 0x111, 0xf, 0xf, false));   // row_shr:1
+  v = f(v, __builtin_amdgcn_update_dpp(identity, v, 0x112, 0xf, 0xf, false));   // row_shr:2
+  v = f(v, __builtin_amdgcn_update_dpp(identity, v, 0x114, 0xf, 0xf, false));   // row_shr:4
+  v = f(v, __builtin_amdgcn_update_dpp(identity, v, 0x118, 0xf, 0xf, false));   // row_shr:8
+  v = f(v, __builtin_amdgcn_update_dpp(identity, v, 0x142, 0xa, 0xf, false));   // row_bcast:15
+  v = f(v, __builtin_amdgcn_update_dpp(identity, v, 0x143, 0xc, 0xf, false));   // row_bcast:31
+  return v;
+}
+
+// The slot-th tile of `tok` rows over the experts' segments (tile_walk.h's bounds: the
+// offsets are not trusted).  Every wavefront scans for itself, 64 experts a step: a
+// running maximum of the offsets and a running sum of the experts' tiles.
+__device__ __forceinline__ TokenTile find_tile(const int32_t* offsets, int E, int64_t n_max, int tok, int slot) {
   const int lane = threadIdx.x & 63;
-  int prev = offsets[0];
-  int base = 0;
+  int prev = offsets[0], base = 0;
   for (int e0 = 0; e0 < E; e0 += 64) {
     const int e = e0 + lane;
-    int top = e < E ? offsets[e + 1] : prev;
-    top = top > prev ? top : prev;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int v = __shfl_up(top, o, 64);
-      if (lane >= o && v > top) top = v;
-    }
+    const int raw = e < E ? offsets[e + 1] : prev;
+    const int top = lane_scan(raw > prev ? raw : prev, INT32_MIN, [](int a, int b) { return a > b ? a : b; });
     int below = __shfl_up(top, 1, 64);
     if (lane == 0) below = prev;
     const int hi = (int)clamp64(top, 0, n_max), lo = (int)clamp64(below, 0, n_max);
-    int sum = e < E ? (hi - lo + kTok - 1) / kTok : 0;
-    const int own = sum;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int v = __shfl_up(sum, o, 64);
-      if (lane >= o) sum += v;
-    }
+    const int own = e < E ? (hi - lo + tok - 1) / tok : 0;
+    const int sum = lane_scan(own, 0, [](int a, int b) { return a + b; });
     const unsigned long long past = __ballot(base + sum > slot);
     if (past != 0) {
       const int src = __ffsll(past) - 1;
-      const int t = slot - base - __shfl(sum - own, src, 64);
-      const int l = __shfl(lo, src, 64), h = __shfl(hi, src, 64);
-      const int left = h - l - t * kTok;
-      return {e0 + src, (int64_t)l + (int64_t)t * kTok, left < kTok ? left : kTok};
+      const int t = slot - base - (__builtin_amdgcn_readlane(sum, src) - __builtin_amdgcn_readlane(own, src));
+      const int row0 = __builtin_amdgcn_readlane(lo, src) + t * tok;
+      const int left = __builtin_amdgcn_readlane(hi, src) - row0;
+      return {e0 + src, row0, left < tok ? left : tok};
     }
-    base += __shfl(sum, 63, 64);
-    prev = __shfl(top, 63, 64);
+    base += __builtin_amdgcn_readlane(sum, 63);
+    prev = __builtin_amdgcn_readlane(top, 63);
   }
   return {-1, 0, 0};
 }
 
 // Eight codes -> eight bf16: 128 + q in elements 0 and 1, 16 + q in the others; FINE:
 // 16 + q throughout (one shift more; the smaller offset keeps four times less rounding
-// of the group sums, which float32 results show and bf16 ones do not).
-template <bool FINE> __device__ __forceinline__ bf16x8 unpack(uint32_t u) {
+// of the group sums, which float32 results show and bf16 ones do not).  The constants are
+// registers (as literals, of which an instruction holds one, each and-or became two
+// instructions): the masks vector ones, the exponents scalar ones.
+struct UnpackConstants {
+  uint32_t mask0, mask3, exp7, exp4;
+  __device__ __forceinline__ UnpackConstants() : mask0(0x000f000fu), mask3(0x00780078u), exp7(0x43004300u), exp4(0x41804180u) {
+    asm("" : "+v"(mask0), "+v"(mask3), "+s"(exp7), "+s"(exp4));
+  }
+};
+template <bool FINE> __device__ __forceinline__ bf16x8 unpack(uint32_t u, const UnpackConstants& k) {
   u32x4 v;
-  v[0] = FINE ? ((u << 3) & 0x00780078u) | 0x41804180u : (u & 0x000f000fu) | 0x43004300u;
-  v[1] = ((u >> 1) & 0x00780078u) | 0x41804180u;
-  v[2] = ((u >> 5) & 0x00780078u) | 0x41804180u;
-  v[3] = ((u >> 9) & 0x00780078u) | 0x41804180u;
+  v[0] = FINE ? ((u << 3) & k.mask3) | k.exp4 : (u & k.mask0) | k.exp7;
+  v[1] = ((u >> 1) & k.mask3) | k.exp4;
+  v[2] = ((u >> 5) & k.mask3) | k.exp4;
+  v[3] = ((u >> 9) & k.mask3) | k.exp4;
   return __builtin_bit_cast(bf16x8, v);
 }
 template <bool FINE> __device__ __forceinline__ bf16x8 offset_operand() {
@@ -117,140 +161,367 @@ __device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
-// GPT scales of four rows each
-template <int GPT> struct Scales {
-  uint2 v[GPT];
+// A buffer whose loads at offsets of `bytes` and more give zero and touch no memory.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t bounded(const void* p, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00027000);
+}
+constexpr uint32_t kNowhere = 0xfffffff0u;   // an offset past every buffer
+__device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t more) {
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, (int)more, 0));
+}
+
+// `bytes` (2, 4 or 8) at offset `at` of a buffer, in a pair of words
+template <int BYTES> __device__ __forceinline__ uint2 load_scales(__amdgpu_buffer_rsrc_t r, int at) {
+  if constexpr (BYTES == 8) return __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(r, at, 0, 0));
+  else if constexpr (BYTES == 4) return uint2{__builtin_amdgcn_raw_buffer_load_b32(r, at, 0, 0), 0u};
+  else return uint2{(uint32_t)__builtin_amdgcn_raw_buffer_load_b16(r, at, 0, 0), 0u};
+}
+__device__ __forceinline__ float scale_at(const uint2& v, int i) {
+  const uint32_t u = i < 2 ? v.x : v.y;
+  return __uint_as_float(i & 1 ? u & 0xffff0000u : u << 16);
+}
+
+// A wavefront's LDS accesses are carried out in order; this keeps the compiler to it.
+__device__ __forceinline__ void lds_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+// A workgroup barrier for LDS: loads into registers stay in flight.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// How the planes of a tile's rows are laid over MFMA rows.  Where SLOT rows of each plane
+// fit 16 together they share one MFMA (plane p of row r is MFMA row p * SLOT + r, and the
+// planes' results are added at the end); with SLOT 16 each plane has MFMAs of its own, which
+// follow one another into the same accumulators, and there may be CT tiles of 16 rows.
+template <int PLANES, int SLOT, int CT> struct Rows {
+  static constexpr bool kPacked = PLANES * SLOT <= 16;
+  static constexpr int kMfma = kPacked ? 1 : PLANES;          // planes that follow one another
+  static constexpr int kGroups = kPacked ? PLANES * SLOT / 4 : 4 * CT;   // groups of four rows of one load unit
+  static constexpr int kTile = kMfma * CT * 4096;             // LDS bytes of 128 columns
+  static constexpr int kUnits = kMfma;                        // load units of a column tile
+  static_assert(CT == 1 || !kPacked || PLANES == 1);
 };
 
-// PLANES bf16 planes of x; GPT groups a tile; SWIGLU: the two streams are the same
-// rows of the gate and up matrices and y gets silu(g) * u in OUT planes; otherwise
-// they are two adjacent row tiles of one matrix and y gets the products as TO.
-template <int PLANES, int GPT, bool SWIGLU, int OUT, typename TO>
-__global__ __launch_bounds__(64 * kWaves) void w4_matvec_kernel(W4Args a) {
-  __shared__ float red[kWaves][2][16][kTok + 1];
-  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
-  const int col = lane & 15, quad = lane >> 4;
-  constexpr bool FINE = PLANES == 3;
-
-  TokenTile tt;
-  if (a.offsets) {
-    tt = find_tile(a.offsets, a.E, a.n_max, (int)blockIdx.y);
-    if (tt.e < 0) return;
-  } else {
-    const int64_t r0 = (int64_t)blockIdx.y * kTok, left = a.n_max - r0;
-    tt = {0, r0, left < kTok ? (int)left : kTok};
+// Activations go through LDS: a lane's MFMA operand is 16 bytes of row lane%16, and loaded
+// like that straight into registers every load instruction touches 64 separate pieces,
+// which costs the address unit as much as 1 KB of weights (measured at 5 rows an expert:
+// 210 us against 182 without these loads).  Instead a load takes 256 contiguous bytes of
+// each of four rows, one write puts them down and four reads pick the operands up.  Piece j
+// of row r lies at j ^ r, so that the 16 rows of a read are in 16 different bank groups.
+template <int PLANES, int SLOT, int CT> struct RowLoads {
+  using L = Rows<PLANES, SLOT, CT>;
+  static constexpr int RG = L::kGroups;
+  __amdgpu_buffer_rsrc_t xr;
+  uint32_t off[RG], last[RG];        // in the last column tile, columns past the row are not there either
+  uint32_t plane;                    // bytes between planes
+  int put[RG], KT;
+  __device__ __forceinline__ RowLoads(const W4Args& a, int row0, int rows) : KT(a.KT) {
+    const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4;
+    const bool cut = (a.KT - 1) * kW4Cols + col * 8 >= a.C;
+    plane = (uint32_t)a.n_in * (uint32_t)(a.C * 2);
+    xr = bounded(a.x, plane * PLANES);
+#pragma unroll
+    for (int g = 0; g < RG; ++g) {
+      const int v = g * 4 + quad, r = L::kPacked ? v % SLOT : v;
+      off[g] = kNowhere;             // rows that are not there load nothing, and so zeros
+      if (r < rows)
+        off[g] = (uint32_t)(a.a_rows ? clamp_row(a.a_rows[row0 + r], a.n_in) : row0 + r) * (uint32_t)(a.C * 2) +
+                 col * 16 + (L::kPacked ? v / SLOT * plane : 0u);
+      last[g] = cut ? kNowhere : off[g];
+      put[g] = v * 256 + ((col ^ (v & 15)) * 16);
+    }
   }
-  const int e = __builtin_amdgcn_readfirstlane(tt.e), rows = __builtin_amdgcn_readfirstlane(tt.rows);
-  const int64_t row0 = tt.row0;
+  // unit u of column tile k, clamped to the row's
+  __device__ __forceinline__ void load(u32x4 (&x)[RG], int u, int k) const {
+    const int kc = k < KT ? k : KT - 1;
+#pragma unroll
+    for (int g = 0; g < RG; ++g) x[g] = load16(xr, kc == KT - 1 ? last[g] : off[g], u * plane + kc * (kW4Cols * 2));
+  }
+  __device__ __forceinline__ void store(const u32x4 (&x)[RG], int u, char* tile) const {
+#pragma unroll
+    for (int g = 0; g < RG; ++g) *reinterpret_cast<u32x4*>(tile + u * (CT * 4096) + put[g]) = x[g];
+  }
+};
 
-  // the streams' row tiles; a second tile past the matrix reads the first again and is not stored
-  const int rt0 = SWIGLU ? (int)blockIdx.x : 2 * (int)blockIdx.x;
-  const int rt1 = SWIGLU ? rt0 : (rt0 + 1 < a.RT ? rt0 + 1 : rt0);
-  const int64_t t0 = ((int64_t)e * a.RT + rt0) * a.KT, t1 = ((int64_t)e * a.RT + rt1) * a.KT;
-  const uint32_t* codes[2] = {a.codes[0] + t0 * 256 + lane * 4, a.codes[SWIGLU ? 1 : 0] + t1 * 256 + lane * 4};
-  const uint16_t* scales[2] = {a.scales[0] + t0 * (16 * GPT) + quad * (4 * GPT),
-                               a.scales[SWIGLU ? 1 : 0] + t1 * (16 * GPT) + quad * (4 * GPT)};
-  // lanes past the last row repeat it: a column of the result depends on its own column of B only
-  const int64_t r = row0 + (col < rows ? col : rows - 1);
-  const int64_t src = a.a_rows ? clamp_row(a.a_rows[r], a.n_in) : r;
-  const bf16* x = a.x + src * (int64_t)a.C + quad * 8;
+// One column tile of NT streams of weights against an LDS tile of rows.  s holds the scales
+// of the streams' groups, this tile's from group s_at on.
+template <int MP, bool FINE, int GPT, int CT, int NT>
+__device__ __forceinline__ void multiply_tile(const char* tile, const u32x4 (&w)[NT], const uint2 (&s)[NT], int s_at,
+                                              bf16x8 minus, const UnpackConstants& consts, f32x4 (&total)[NT][CT]) {
+  constexpr int M = 4 / GPT;         // MFMAs of a group
+  const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4;
+  bf16x8 b[CT][MP][4];
+#pragma unroll
+  for (int c = 0; c < CT; ++c)
+#pragma unroll
+    for (int p = 0; p < MP; ++p)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        b[c][p][i] = *reinterpret_cast<const bf16x8*>(tile + p * (CT * 4096) + c * 4096 + col * 256 +
+                                                      (((i * 4 + quad) ^ col) * 16));
+#pragma unroll
+  for (int g = 0; g < GPT; ++g) {
+    f32x4 c0[CT];
+#pragma unroll
+    for (int c = 0; c < CT; ++c) {
+      c0[c] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = g * M; i < (g + 1) * M; ++i)
+#pragma unroll
+        for (int p = 0; p < MP; ++p) c0[c] = mfma(b[c][p][i], minus, c0[c]);
+    }
+#pragma unroll
+    for (int m = 0; m < NT; ++m) {
+      f32x4 acc[CT];
+#pragma unroll
+      for (int c = 0; c < CT; ++c) acc[c] = c0[c];
+#pragma unroll
+      for (int i = g * M; i < (g + 1) * M; ++i) {
+        const bf16x8 wf = unpack<FINE>(w[m][i], consts);
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+#pragma unroll
+          for (int p = 0; p < MP; ++p) acc[c] = mfma(b[c][p][i], wf, acc[c]);
+      }
+      const float sc = scale_at(s[m], s_at + g);
+#pragma unroll
+      for (int c = 0; c < CT; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) total[m][c][i] = fmaf(sc, acc[c][i], total[m][c][i]);
+    }
+  }
+  // the sums are due here: moved behind the loop's other tiles they would keep every
+  // group's accumulators alive
+#pragma unroll
+  for (int m = 0; m < NT; ++m)
+#pragma unroll
+    for (int c = 0; c < CT; ++c) asm volatile("" : "+v"(total[m][c]));
+}
 
-  f32x4 total[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+// The buffers of one set of NT streams.  SWIGLU: row tiles of the gate and up matrices in
+// turn; otherwise adjacent row tiles of one matrix.  A stream past the matrix has no bytes:
+// it loads zeros, and its scales with them.
+template <int NT, int GPT, bool SWIGLU> struct Streams {
+  __amdgpu_buffer_rsrc_t codes[NT], scales[NT];
+  int n, NG;
+  // from column tile k0 on, n of them
+  __device__ __forceinline__ Streams(const W4Args& a, int64_t e, int first, int k0, int n_) : n(n_), NG(a.NG) {
+#pragma unroll
+    for (int m = 0; m < NT; ++m) {
+      const int rt = first + (SWIGLU ? m / 2 : m), mat = SWIGLU ? m % 2 : 0;
+      const bool in = rt < a.RT;
+      const int64_t t = e * a.RT + (in ? rt : 0);
+      codes[m] = bounded(a.codes[mat] + (t * a.KT + k0) * 256, in ? n * 1024 : 0);
+      scales[m] = bounded(a.scales[mat] + t * 16 * NG + k0 * GPT, in ? (16 * NG - k0 * GPT) * 2 : 0);
+    }
+  }
+  __device__ __forceinline__ void load(u32x4 (&w)[NT], int k) const {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int m = 0; m < NT; ++m)
+      w[m] = __builtin_bit_cast(
+          u32x4, __builtin_amdgcn_raw_buffer_load_b128(codes[m], lane * 16 + k * 1024, 0, kStreamed));
+  }
+  // of SB column tiles from k on; zeros past the n-th
+  template <int SB> __device__ __forceinline__ void load_scales_of(uint2 (&s)[NT], int k) const {
+    const int col = threadIdx.x & 15;
+#pragma unroll
+    for (int m = 0; m < NT; ++m)
+      s[m] = load_scales<SB * GPT * 2>(scales[m], k < n ? col * (NG * 2) + k * (GPT * 2) : (int)kNowhere);
+  }
+};
+
+// The products of a set of streams' n column tiles from k0 on, DEPTH of them in flight (a
+// multiplication past the n-th adds zero: its scales are).
+//
+// SHARED: the workgroup's wavefronts go over the same columns, and each puts down one load
+// unit of the next kWaves for all: a quarter of the loads, and one barrier for them (it waits
+// for LDS only, the weights stay in flight).  Otherwise a wavefront has columns and LDS of
+// its own.
+template <int PLANES, int SLOT, int CT, int GPT, int NT, int DEPTH, bool SHARED, bool SWIGLU>
+__device__ __forceinline__ void stream(const W4Args& a, const Streams<NT, GPT, SWIGLU>& from, int k0, int row0, int rows,
+                                       char* lds, f32x4 (&total)[NT][CT]) {
+  using L = Rows<PLANES, SLOT, CT>;
+  constexpr bool FINE = PLANES == 3;
+  constexpr int SB = 4 / GPT < DEPTH ? 4 / GPT : DEPTH;       // column tiles of a scale load
+  const RowLoads<PLANES, SLOT, CT> rl(a, row0, rows);
   const bf16x8 minus = offset_operand<FINE>();
-  for (int k0 = wave; k0 < a.KT; k0 += kWaves * kDepth) {
-    u32x4 w[kDepth][2];
-    Scales<GPT> s[kDepth][2];
-    bf16x8 b[kDepth][PLANES][4];
+  const UnpackConstants consts;
+  u32x4 w[DEPTH][NT];
+  uint2 s[DEPTH / SB][NT];
+  if constexpr (SHARED) {
+    constexpr int CH = kWaves / L::kUnits, U = DEPTH > CH ? DEPTH : CH;     // column tiles of a chunk, of a turn
+    static_assert(U % CH == 0 && U % DEPTH == 0);
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int tile = wave / L::kUnits, unit = wave % L::kUnits;
+    u32x4 x[L::kGroups];
+    auto put = [&](int half) {
+      if (tile < CH) rl.store(x, unit, lds + (half * CH + tile) * L::kTile);
+      lds_barrier();
+    };
+    rl.load(x, unit, tile);
 #pragma unroll
-    for (int u = 0; u < kDepth; ++u) {
-      const int kt = k0 + u * kWaves < a.KT ? k0 + u * kWaves : k0;
-#pragma unroll
-      for (int n = 0; n < 2; ++n) w[u][n] = *reinterpret_cast<const u32x4*>(codes[n] + (int64_t)kt * 256);
+    for (int u = 0; u < DEPTH; ++u) {
+      from.load(w[u], u);
+      if (u % SB == 0) from.template load_scales_of<SB>(s[u / SB], u);
     }
+    put(0);
+    int half = 0;
+    for (int k = 0; k < from.n; k += U) {
 #pragma unroll
-    for (int u = 0; u < kDepth; ++u) {
-      const int kt = k0 + u * kWaves < a.KT ? k0 + u * kWaves : k0;
-#pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int g = 0; g < GPT; ++g)
-          s[u][n].v[g] = *reinterpret_cast<const uint2*>(scales[n] + (int64_t)kt * (16 * GPT) + g * 4);
-#pragma unroll
-      for (int p = 0; p < PLANES; ++p)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          // columns past the row: any in-bounds value; their scale is 0 or their MFMA is skipped
-          const int c = kt * kW4Cols + i * 32 < a.C ? kt * kW4Cols + i * 32 : 0;
-          b[u][p][i] = *reinterpret_cast<const bf16x8*>(x + p * a.x_plane + c);
-        }
+      for (int v = 0; v < U; ++v) {
+        const int u = v % DEPTH;
+        if (v % CH == 0) rl.load(x, unit, k + v + CH + tile);
+        multiply_tile<L::kMfma, FINE, GPT, CT, NT>(lds + (half * CH + v % CH) * L::kTile, w[u], s[u / SB],
+                                                   u % SB * GPT, minus, consts, total);
+        from.load(w[u], k + v + DEPTH);
+        if (u % SB == SB - 1) from.template load_scales_of<SB>(s[u / SB], k + v + 1 - SB + DEPTH);
+        if (v % CH == CH - 1) put(half ^= 1);  // the other half was last read before the last barrier
+        W4_SCHED;
+      }
     }
+  } else {
+    u32x4 x[DEPTH][L::kUnits][L::kGroups];
 #pragma unroll
-    for (int u = 0; u < kDepth; ++u) {
-      const int kt = k0 + u * kWaves;
-      if (kt >= a.KT) break;
+    for (int u = 0; u < DEPTH; ++u) {
+      from.load(w[u], u);
 #pragma unroll
-      for (int g = 0; g < GPT; ++g) {
-        constexpr int M = 4 / GPT;      // MFMAs of a group
-        f32x4 c0 = {0.f, 0.f, 0.f, 0.f};
+      for (int p = 0; p < L::kUnits; ++p) rl.load(x[u][p], p, k0 + u);
+      if (u % SB == 0) from.template load_scales_of<SB>(s[u / SB], u);
+    }
+    for (int k = 0; k < from.n; k += DEPTH) {
 #pragma unroll
-        for (int m = 0; m < M; ++m) {
-          const int i = g * M + m;
-          if (kt * kW4Cols + i * 32 >= a.C) break;
+      for (int u = 0; u < DEPTH; ++u) {
+        lds_order();                           // the operands before these have been read
 #pragma unroll
-          for (int p = 0; p < PLANES; ++p) c0 = mfma(minus, b[u][p][i], c0);
-        }
+        for (int p = 0; p < L::kUnits; ++p) rl.store(x[u][p], p, lds);
+        lds_order();
+        multiply_tile<L::kMfma, FINE, GPT, CT, NT>(lds, w[u], s[u / SB], u % SB * GPT, minus, consts, total);
+        from.load(w[u], k + u + DEPTH);
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          f32x4 acc = c0;
-#pragma unroll
-          for (int m = 0; m < M; ++m) {
-            const int i = g * M + m;
-            if (kt * kW4Cols + i * 32 >= a.C) break;
-            const bf16x8 wf = unpack<FINE>(w[u][n][i]);
-#pragma unroll
-            for (int p = 0; p < PLANES; ++p) acc = mfma(wf, b[u][p][i], acc);
-          }
-          const uint2 sv = s[u][n].v[g];
-          total[n][0] = fmaf(__uint_as_float(sv.x << 16), acc[0], total[n][0]);
-          total[n][1] = fmaf(__uint_as_float(sv.x & 0xffff0000u), acc[1], total[n][1]);
-          total[n][2] = fmaf(__uint_as_float(sv.y << 16), acc[2], total[n][2]);
-          total[n][3] = fmaf(__uint_as_float(sv.y & 0xffff0000u), acc[3], total[n][3]);
-        }
+        for (int p = 0; p < L::kUnits; ++p) rl.load(x[u][p], p, k0 + k + u + DEPTH);
+        if (u % SB == SB - 1) from.template load_scales_of<SB>(s[u / SB], k + u + 1 - SB + DEPTH);
+        W4_SCHED;
       }
     }
   }
-
+  // planes that shared MFMAs: their results are SLOT rows apart
+  if constexpr (L::kPacked && PLANES > 1) {
+    const int quad = (threadIdx.x & 63) >> 4;
 #pragma unroll
-  for (int n = 0; n < 2; ++n)
+    for (int m = 0; m < NT; ++m)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) red[wave][n][quad * 4 + i][col] = total[n][i];
-  __syncthreads();
-
-  const int ro = tid & 15, tok = tid >> 4;      // one result (of each stream) a thread
-  float v[2];
-#pragma unroll
-  for (int n = 0; n < 2; ++n) {
-    v[n] = red[0][n][ro][tok];
-#pragma unroll
-    for (int q = 1; q < kWaves; ++q) v[n] += red[q][n][ro][tok];
+      for (int i = 0; i < 4; ++i) {
+        float v = quad * 4 < PLANES * SLOT ? total[m][0][i] : 0.f;
+        if (SLOT == 4) v += __shfl_xor(v, 16, 64);
+        if (PLANES * SLOT > 8) v += __shfl_xor(v, 32, 64);
+        total[m][0][i] = v;
+      }
   }
-  if (tok >= rows) return;
-  if constexpr (SWIGLU) {
-    const int f = rt0 * kW4Rows + ro;
-    if (f >= a.R) return;
-    float h = v[0] / (1.f + expf(-v[0])) * v[1];
-    bf16* y = static_cast<bf16*>(a.y) + (row0 + tok) * (int64_t)a.R + f;
+}
+
+// The results of one set of streams and 16 token rows.
+template <int NT, bool SWIGLU, int OUT, typename TO>
+__device__ __forceinline__ void store_results(const W4Args& a, const f32x4 (&v)[NT], int first, int64_t row0, int rows) {
+  constexpr int kRows = SWIGLU ? NT / 2 : NT;
+  const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4;
 #pragma unroll
-    for (int p = 0; p < OUT; ++p) {
-      const bf16 part = from_f32<bf16>(h);
-      y[p * a.y_plane] = part;
-      h -= to_f32(part);
+  for (int i = 0; i < 4; ++i) {
+    if (quad * 4 + i >= rows) continue;
+    const int64_t row = (row0 + quad * 4 + i) * a.R;
+#pragma unroll
+    for (int m = 0; m < kRows; ++m) {
+      const int f = (first + m) * kW4Rows + col;
+      if (f >= a.R) continue;
+      if constexpr (SWIGLU) {
+        const float g = v[2 * m][i];
+        float h = g / (1.f + expf(-g)) * v[2 * m + 1][i];
+#pragma unroll
+        for (int p = 0; p < OUT; ++p) {
+          const bf16 part = from_f32<bf16>(h);
+          static_cast<bf16*>(a.y)[p * a.y_plane + row + f] = part;
+          h -= to_f32(part);
+        }
+      } else {
+        static_cast<TO*>(a.y)[row + f] = from_f32<TO>(v[m][i]);
+      }
     }
+  }
+}
+
+// Up to CT * 16 token rows a workgroup (blockIdx.y) and some of the weight rows: KS
+// wavefronts share a set of NT streams, each a run of their column tiles.
+template <int PLANES, int GPT, int CT, int KS, int NT, int DEPTH, bool SWIGLU, int OUT, typename TO>
+__global__ __launch_bounds__(64 * kWaves, W4_OCC) void w4_matvec_kernel(W4Args a) {
+  constexpr int kRows = SWIGLU ? NT / 2 : NT;                 // row tiles of a set
+  constexpr bool kShared = KS == 1;
+  // LDS: two chunks of column tiles, or one column tile a wavefront
+  constexpr int kTile = Rows<PLANES, 16, CT>::kTile, kPack = 4096 * CT;
+  constexpr int kLds = kShared ? 2 * (kWaves / PLANES * kTile > kWaves * kPack ? kWaves / PLANES * kTile : kWaves * kPack)
+                               : kWaves * kTile;
+  constexpr int kRed = KS > 1 ? kWaves * NT * CT * 1024 : 0;
+  __shared__ __attribute__((aligned(16))) char lds[kLds > kRed ? kLds : kRed];
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), lane = threadIdx.x & 63;
+
+  TokenTile tt;
+  if (a.offsets) {
+    tt = find_tile(a.offsets, a.E, a.n_max, CT * kTok, (int)blockIdx.y);
+    if (tt.e < 0) return;
   } else {
-    TO* y = static_cast<TO*>(a.y) + (row0 + tok) * (int64_t)a.R;
-    const int n0 = rt0 * kW4Rows + ro, n1 = (rt0 + 1) * kW4Rows + ro;
-    if (n0 < a.R) y[n0] = from_f32<TO>(v[0]);
-    if (n1 < a.R) y[n1] = from_f32<TO>(v[1]);
+    const int64_t r0 = (int64_t)blockIdx.y * (CT * kTok), left = a.n_max - r0;
+    tt = {0, (int)r0, left < CT * kTok ? (int)left : CT * kTok};
+  }
+  const int64_t e = __builtin_amdgcn_readfirstlane(tt.e);
+  const int row0 = __builtin_amdgcn_readfirstlane(tt.row0), rows = __builtin_amdgcn_readfirstlane(tt.rows);
+
+  const int first = ((int)blockIdx.x * (kWaves / KS) + wave / KS) * kRows;      // row tile of stream 0
+  // this wavefront's run of column tiles: whole scale loads
+  constexpr int SB = 4 / GPT < DEPTH ? 4 / GPT : DEPTH;
+  const int run = ((a.KT + KS - 1) / KS + SB - 1) / SB * SB, k0 = (wave % KS) * run;
+  const int n = (!kShared && first >= a.RT) || k0 >= a.KT ? 0 : (a.KT - k0 < run ? a.KT - k0 : run);
+  f32x4 total[NT][CT];
+#pragma unroll
+  for (int m = 0; m < NT; ++m)
+#pragma unroll
+    for (int c = 0; c < CT; ++c) total[m][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+  if (n > 0) {
+    const Streams<NT, GPT, SWIGLU> from(a, e, first, k0, n);
+    char* mine = kShared ? lds : lds + wave * kTile;
+    if (CT == 1 && rows <= 4)
+      stream<PLANES, CT == 1 ? 4 : 16, CT, GPT, NT, DEPTH, kShared>(a, from, k0, row0, rows, mine, total);
+    else if (CT == 1 && PLANES < 3 && rows <= 8)
+      stream<PLANES, CT == 1 && PLANES < 3 ? 8 : 16, CT, GPT, NT, DEPTH, kShared>(a, from, k0, row0, rows, mine, total);
+    else
+      stream<PLANES, 16, CT, GPT, NT, DEPTH, kShared>(a, from, k0, row0, rows, mine, total);
+  }
+
+  f32x4* red = reinterpret_cast<f32x4*>(lds);                 // [wave][NT][CT][lane]
+  if constexpr (KS > 1) {
+    __syncthreads();
+#pragma unroll
+    for (int m = 0; m < NT; ++m)
+#pragma unroll
+      for (int c = 0; c < CT; ++c) red[((wave * NT + m) * CT + c) * 64 + lane] = total[m][c];
+    __syncthreads();
+  }
+  if (first >= a.RT) return;
+#pragma unroll
+  for (int c = 0; c < CT; ++c) {
+    if (KS > 1 && c % KS != wave % KS) continue;
+    f32x4 v[NT];
+#pragma unroll
+    for (int m = 0; m < NT; ++m) {
+      v[m] = total[m][c];
+      if constexpr (KS > 1) {
+        const int w0 = wave - wave % KS;
+        v[m] = red[((w0 * NT + m) * CT + c) * 64 + lane];
+#pragma unroll
+        for (int q = 1; q < KS; ++q) v[m] += red[(((w0 + q) * NT + m) * CT + c) * 64 + lane];
+      }
+    }
+    store_results<NT, SWIGLU, OUT, TO>(a, v, first, row0 + c * kTok, rows - c * kTok);
   }
 }
 
@@ -271,15 +542,29 @@ __global__ __launch_bounds__(256) void split3_kernel(int64_t n, const float* __r
   }
 }
 
+template <int PLANES, int GPT, int CT, int KS, int NT, bool SWIGLU, int OUT, typename TO>
+void launch_one(const W4Args& a, hipStream_t stream, int64_t token_tiles) {
+  constexpr int DEPTH = KS == 1 ? 4 : PLANES == 1 ? W4_D1 : W4_D2;
+  const int per = kWaves / KS * (SWIGLU ? NT / 2 : NT);       // row tiles of a workgroup
+  hipLaunchKernelGGL((w4_matvec_kernel<PLANES, GPT, CT, KS, NT, DEPTH, SWIGLU, OUT, TO>),
+                     dim3((unsigned)((a.RT + per - 1) / per), (unsigned)token_tiles), dim3(64 * kWaves), 0, stream, a);
+}
+
+template <int PLANES, int GPT, bool SWIGLU, int OUT, typename TO>
+void launch_group(const W4Args& a, int num_cu, hipStream_t stream) {
+  const int64_t tiles = a.offsets ? w4_token_tiles(a.n_max, a.E) : (a.n_max + kTok - 1) / kTok;
+  const int64_t busy = a.offsets ? (a.n_max < a.E ? a.n_max : a.E) : tiles;    // tiles with rows, about
+  const int64_t waves = a.RT / (SWIGLU ? 2 : 4) * busy;
+  if (waves >= (int64_t)num_cu * W4_FULL)
+    launch_one<PLANES, GPT, 1, 1, SWIGLU ? W4_NTM : W4_NTMD, SWIGLU, OUT, TO>(a, stream, tiles);
+  else launch_one<PLANES, GPT, 1, SWIGLU ? W4_KSU : W4_KSD, SWIGLU ? W4_NTU : W4_NTD, SWIGLU, OUT, TO>(a, stream, tiles);
+}
+
 template <int PLANES, bool SWIGLU, int OUT, typename TO>
-hipError_t launch(const W4Args& a, int group, int64_t token_tiles, hipStream_t stream) {
-  const dim3 grid((unsigned)(SWIGLU ? a.RT : (a.RT + 1) / 2), (unsigned)token_tiles), block(64 * kWaves);
-  if (group == 32)
-    hipLaunchKernelGGL((w4_matvec_kernel<PLANES, 4, SWIGLU, OUT, TO>), grid, block, 0, stream, a);
-  else if (group == 64)
-    hipLaunchKernelGGL((w4_matvec_kernel<PLANES, 2, SWIGLU, OUT, TO>), grid, block, 0, stream, a);
-  else
-    hipLaunchKernelGGL((w4_matvec_kernel<PLANES, 1, SWIGLU, OUT, TO>), grid, block, 0, stream, a);
+hipError_t launch(const W4Args& a, int group, int num_cu, hipStream_t stream) {
+  if (group == 32) launch_group<PLANES, 4, SWIGLU, OUT, TO>(a, num_cu, stream);
+  else if (group == 64) launch_group<PLANES, 2, SWIGLU, OUT, TO>(a, num_cu, stream);
+  else launch_group<PLANES, 1, SWIGLU, OUT, TO>(a, num_cu, stream);
   return hipGetLastError();
 }
 
@@ -297,55 +582,53 @@ int64_t w4_token_tiles(int64_t n_max, int64_t E) {
 }
 
 hipError_t launch_w4_matvec(int dtype, int64_t T, int64_t C, int64_t R, int group, const void* x, const void* codes,
-                            const void* scales, void* y, void* x_planes, hipStream_t stream) {
+                            const void* scales, void* y, void* x_planes, int num_cu, hipStream_t stream) {
   W4Args a{};
   a.n_in = a.n_max = T;
   a.E = 1;
   a.C = (int)C; a.R = (int)R; a.KT = (int)w4_col_tiles(C); a.RT = (int)w4_row_tiles(R);
+  a.NG = w4_row_scales(C, group);
   a.codes[0] = (const uint32_t*)codes; a.scales[0] = (const uint16_t*)scales;
   a.y = y;
-  const int64_t tiles = (T + kTok - 1) / kTok;
   if (dtype == 1) {
     a.x = (const bf16*)x;
-    return launch<1, false, 1, bf16>(a, group, tiles, stream);
+    return launch<1, false, 1, bf16>(a, group, num_cu, stream);
   }
   hipError_t err = launch_split3(T * C, x, x_planes, stream);
   if (err != hipSuccess) return err;
   a.x = (const bf16*)x_planes;
-  a.x_plane = T * C;
-  return launch<3, false, 1, float>(a, group, tiles, stream);
+  return launch<3, false, 1, float>(a, group, num_cu, stream);
 }
 
 hipError_t launch_w4_grouped_ffn(int dtype, int64_t n_max, int64_t d, int64_t E, int64_t F, int group, const void* x,
                                  int64_t n_in, const int32_t* a_rows, const int32_t* offsets, const void* const* codes,
                                  const void* const* scales, void* y_perm, void* x_planes, void* h_planes,
-                                 hipStream_t stream) {
-  const int64_t tiles = w4_token_tiles(n_max, E);
+                                 int num_cu, hipStream_t stream) {
   W4Args g{};
   g.n_in = n_in; g.a_rows = a_rows; g.offsets = offsets; g.n_max = n_max;
   g.E = (int)E;
   g.C = (int)d; g.R = (int)F; g.KT = (int)w4_col_tiles(d); g.RT = (int)w4_row_tiles(F);
   for (int n = 0; n < 2; ++n) { g.codes[n] = (const uint32_t*)codes[n]; g.scales[n] = (const uint16_t*)scales[n]; }
+  g.NG = w4_row_scales(d, group);
   g.y = h_planes;
   g.y_plane = n_max * F;
   W4Args w = g;
   w.x = (const bf16*)h_planes;
-  w.x_plane = n_max * F;
   w.n_in = n_max; w.a_rows = nullptr;
   w.C = (int)F; w.R = (int)d; w.KT = (int)w4_col_tiles(F); w.RT = (int)w4_row_tiles(d);
+  w.NG = w4_row_scales(F, group);
   w.codes[0] = (const uint32_t*)codes[2]; w.scales[0] = (const uint16_t*)scales[2];
   w.y = y_perm;
   hipError_t err;
   if (dtype == 1) {
     g.x = (const bf16*)x;
-    if ((err = launch<1, true, 2, bf16>(g, group, tiles, stream)) != hipSuccess) return err;
-    return launch<2, false, 1, bf16>(w, group, tiles, stream);
+    if ((err = launch<1, true, 2, bf16>(g, group, num_cu, stream)) != hipSuccess) return err;
+    return launch<2, false, 1, bf16>(w, group, num_cu, stream);
   }
   if ((err = launch_split3(n_in * d, x, x_planes, stream)) != hipSuccess) return err;
   g.x = (const bf16*)x_planes;
-  g.x_plane = n_in * d;
-  if ((err = launch<3, true, 3, bf16>(g, group, tiles, stream)) != hipSuccess) return err;
-  return launch<3, false, 1, float>(w, group, tiles, stream);
+  if ((err = launch<3, true, 3, bf16>(g, group, num_cu, stream)) != hipSuccess) return err;
+  return launch<3, false, 1, float>(w, group, num_cu, stream);
 }
 
 }  // namespace moe

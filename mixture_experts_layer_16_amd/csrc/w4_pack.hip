@@ -33,6 +33,17 @@ __device__ __forceinline__ float round_quotient(float w, float s) {
   return q;
 }
 
+// Where the scale of row l%16 and group g of a tile's row tile lies.  The wavefront of the
+// last column tile also clears what pads the row.
+__device__ __forceinline__ int64_t scale_slot(int64_t mat, int RT, int rt, int NG, int lane, int g) {
+  return ((mat * RT + rt) * 16 + (lane & 15)) * NG + g;
+}
+template <int GPT>
+__device__ __forceinline__ void clear_padding(bf16* scales, int64_t mat, int RT, int rt, int KT, int kt, int NG, int lane) {
+  if (kt != KT - 1 || lane >= 16) return;
+  for (int g = KT * GPT; g < NG; ++g) scales[scale_slot(mat, RT, rt, NG, lane, g)] = from_f32<bf16>(0.f);
+}
+
 struct TileAt {
   int64_t mat;     // matrix
   int rt, kt;      // tile in it
@@ -46,7 +57,7 @@ __device__ __forceinline__ TileAt tile_at(int64_t tile, int RT, int KT) {
 // s = bf16(max|w| / 7), q = rint(w / s) + 8 clamped to 0..15; a group whose scale is 0
 // has code 8 throughout.  Reads 2 or 4 bytes and writes half a byte a weight.
 template <typename T, int GPT>
-__global__ __launch_bounds__(256) void w4_quantize_kernel(int64_t tiles, int R, int C, int RT, int KT,
+__global__ __launch_bounds__(256) void w4_quantize_kernel(int64_t tiles, int R, int C, int RT, int KT, int NG,
                                                           const T* __restrict__ w, uint32_t* __restrict__ codes,
                                                           bf16* __restrict__ scales) {
   const int64_t tile = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
@@ -90,15 +101,16 @@ __global__ __launch_bounds__(256) void w4_quantize_kernel(int64_t tiles, int R, 
       q[j] = s > 0.f ? 8 + (int)fminf(fmaxf(round_quotient(v[i][j], s), -8.f), 7.f) : 8;
     words[i] = pack8(q);
     if (quad == 0 && i % (4 / GPT) == 0)
-      scales[tile * (16 * GPT) + ((lane >> 2) * GPT + i / (4 / GPT)) * 4 + (lane & 3)] = sb;
+      scales[scale_slot(at.mat, RT, at.rt, NG, lane, at.kt * GPT + i / (4 / GPT))] = sb;
   }
+  clear_padding<GPT>(scales, at.mat, RT, at.rt, KT, at.kt, NG, lane);
   *reinterpret_cast<u32x4*>(codes + (tile * 64 + lane) * 4) = words;
 }
 
 // Codes given row by row (two a byte, the even column in the low half) and scales
 // [R, ceil(C/group)].
 template <int GPT>
-__global__ __launch_bounds__(256) void w4_pack_kernel(int64_t tiles, int R, int C, int RT, int KT,
+__global__ __launch_bounds__(256) void w4_pack_kernel(int64_t tiles, int R, int C, int RT, int KT, int NG,
                                                       const uint8_t* __restrict__ q, const bf16* __restrict__ s,
                                                       uint32_t* __restrict__ codes, bf16* __restrict__ scales) {
   const int64_t tile = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
@@ -122,16 +134,17 @@ __global__ __launch_bounds__(256) void w4_pack_kernel(int64_t tiles, int R, int 
     words[i] = u;
     if (quad == 0 && i % (4 / GPT) == 0) {
       const int g = at.kt * GPT + i / (4 / GPT);
-      scales[tile * (16 * GPT) + ((lane >> 2) * GPT + i / (4 / GPT)) * 4 + (lane & 3)] =
+      scales[scale_slot(at.mat, RT, at.rt, NG, lane, g)] =
           row < R && g < ng ? s[(at.mat * R + row) * (int64_t)ng + g] : from_f32<bf16>(0.f);
     }
   }
+  clear_padding<GPT>(scales, at.mat, RT, at.rt, KT, at.kt, NG, lane);
   *reinterpret_cast<u32x4*>(codes + (tile * 64 + lane) * 4) = words;
 }
 
 // w = s (q - 8): exact in float32 (12 bits), rounded once for bf16.
 template <typename T, int GPT>
-__global__ __launch_bounds__(256) void w4_dequantize_kernel(int64_t tiles, int R, int C, int RT, int KT,
+__global__ __launch_bounds__(256) void w4_dequantize_kernel(int64_t tiles, int R, int C, int RT, int KT, int NG,
                                                             const uint32_t* __restrict__ codes,
                                                             const uint16_t* __restrict__ scales, T* __restrict__ w) {
   const int64_t tile = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
@@ -144,7 +157,7 @@ __global__ __launch_bounds__(256) void w4_dequantize_kernel(int64_t tiles, int R
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     if (row >= R || c0 + i * 32 >= C) continue;
-    const float s = scale_f32(scales[tile * (16 * GPT) + (((lane & 15) >> 2) * GPT + i / (4 / GPT)) * 4 + (lane & 3)]);
+    const float s = scale_f32(scales[scale_slot(at.mat, RT, at.rt, NG, lane, at.kt * GPT + i / (4 / GPT))]);
     float v[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = s * (float)(code_at(words[i], j) - 8);
@@ -168,10 +181,10 @@ hipError_t launch_w4_quantize(int dtype, int64_t n, int64_t R, int64_t C, int gr
   by_group(group, [&](auto gpt) {
     constexpr int G = decltype(gpt)::value;
     if (dtype == 1)
-      hipLaunchKernelGGL((w4_quantize_kernel<bf16, G>), grid, block, 0, stream, tiles, (int)R, (int)C, RT, KT,
+      hipLaunchKernelGGL((w4_quantize_kernel<bf16, G>), grid, block, 0, stream, tiles, (int)R, (int)C, RT, KT, w4_row_scales(C, group),
                          (const bf16*)w, (uint32_t*)codes, (bf16*)scales);
     else
-      hipLaunchKernelGGL((w4_quantize_kernel<float, G>), grid, block, 0, stream, tiles, (int)R, (int)C, RT, KT,
+      hipLaunchKernelGGL((w4_quantize_kernel<float, G>), grid, block, 0, stream, tiles, (int)R, (int)C, RT, KT, w4_row_scales(C, group),
                          (const float*)w, (uint32_t*)codes, (bf16*)scales);
   });
   return hipGetLastError();
@@ -183,7 +196,7 @@ hipError_t launch_w4_pack(int64_t n, int64_t R, int64_t C, int group, const void
   const int64_t tiles = n * RT * KT;
   const dim3 grid((unsigned)((tiles + 3) / 4)), block(256);
   by_group(group, [&](auto gpt) {
-    hipLaunchKernelGGL((w4_pack_kernel<decltype(gpt)::value>), grid, block, 0, stream, tiles, (int)R, (int)C, RT, KT,
+    hipLaunchKernelGGL((w4_pack_kernel<decltype(gpt)::value>), grid, block, 0, stream, tiles, (int)R, (int)C, RT, KT, w4_row_scales(C, group),
                        (const uint8_t*)q, (const bf16*)s, (uint32_t*)codes, (bf16*)scales);
   });
   return hipGetLastError();
@@ -197,10 +210,10 @@ hipError_t launch_w4_dequantize(int dtype, int64_t n, int64_t R, int64_t C, int 
   by_group(group, [&](auto gpt) {
     constexpr int G = decltype(gpt)::value;
     if (dtype == 1)
-      hipLaunchKernelGGL((w4_dequantize_kernel<bf16, G>), grid, block, 0, stream, tiles, (int)R, (int)C, RT, KT,
+      hipLaunchKernelGGL((w4_dequantize_kernel<bf16, G>), grid, block, 0, stream, tiles, (int)R, (int)C, RT, KT, w4_row_scales(C, group),
                          (const uint32_t*)codes, (const uint16_t*)scales, (bf16*)w);
     else
-      hipLaunchKernelGGL((w4_dequantize_kernel<float, G>), grid, block, 0, stream, tiles, (int)R, (int)C, RT, KT,
+      hipLaunchKernelGGL((w4_dequantize_kernel<float, G>), grid, block, 0, stream, tiles, (int)R, (int)C, RT, KT, w4_row_scales(C, group),
                          (const uint32_t*)codes, (const uint16_t*)scales, (float*)w);
   });
   return hipGetLastError();

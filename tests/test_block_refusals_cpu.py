@@ -118,7 +118,7 @@ def matvec(**kw):
 @pytest.mark.parametrize("want,kw", [
     (INVALID, dict(T=0)), (INVALID, dict(R=0)), (UNSUPPORTED, dict(C=48)), (UNSUPPORTED, dict(group=256)),
     (UNSUPPORTED, dict(dtype=3)), (UNSUPPORTED, dict(T=(1 << 19) + 1)), (UNSUPPORTED, dict(T=1 << 19, R=8192)),
-    (UNSUPPORTED, dict(T=1 << 15, C=1 << 20)), (INVALID, dict(x=None)), (INVALID, dict(x=MIS)),
+    (UNSUPPORTED, dict(T=1 << 15, C=1 << 20)), (UNSUPPORTED, dict(T=1 << 11, C=1 << 20, dtype=1)), (INVALID, dict(x=None)), (INVALID, dict(x=MIS)),
     (INVALID, dict(codes=MIS)), (INVALID, dict(scales=None)), (INVALID, dict(y=None)), (INVALID, dict(ws=MIS)),
     (WORKSPACE, dict(ws=None, n=None)), (WORKSPACE, dict(n=ctypes.byref(ctypes.c_size_t(64))))])
 def test_matvec_refuses(want, kw):
@@ -141,8 +141,8 @@ def ffn(**kw):
 @pytest.mark.parametrize("want,kw", [
     (INVALID, dict(n_max=0)), (INVALID, dict(E=0)), (UNSUPPORTED, dict(E=1025)), (UNSUPPORTED, dict(d=96)),
     (UNSUPPORTED, dict(F=32)), (UNSUPPORTED, dict(group=48)), (UNSUPPORTED, dict(dtype=2)), (INVALID, dict(n_in=0)),
-    (UNSUPPORTED, dict(n_in=1 << 31)), (UNSUPPORTED, dict(n_max=(1 << 19) + 1)),
-    (UNSUPPORTED, dict(n_max=1 << 19, d=1 << 14)), (UNSUPPORTED, dict(E=1024, d=1 << 13, F=1 << 14)),
+    (UNSUPPORTED, dict(n_in=1 << 31)), (UNSUPPORTED, dict(n_in=1 << 24)), (UNSUPPORTED, dict(n_max=(1 << 19) + 1)),
+    (UNSUPPORTED, dict(n_max=1 << 19, d=1 << 14)), (UNSUPPORTED, dict(n_max=1 << 15, F=1 << 16)), (UNSUPPORTED, dict(E=1024, d=1 << 13, F=1 << 14)),
     (INVALID, dict(offsets=None)), (INVALID, dict(x=None)), (INVALID, dict(gc=MIS)), (INVALID, dict(gs=None)),
     (INVALID, dict(uc=None)), (INVALID, dict(us=MIS)), (INVALID, dict(dc=None)), (INVALID, dict(ds=None)),
     (INVALID, dict(y=MIS)), (INVALID, dict(ws=MIS)), (WORKSPACE, dict(ws=None, n=None)),

@@ -95,7 +95,8 @@ def test_pack_holds_the_codes_and_scales(n, R, C, group):
     w, q, s = packed(n, R, C, group, seed=3)
     assert np.array_equal(f64(w.dequantize(FP)), w4o.values(q, s, group))
     RT, KT = -(-R // 16), -(-C // 128)
-    assert w.codes.numel() == n * RT * KT * 1024 and w.scales.numel() == n * RT * KT * 16 * 128 // group
+    NG = -(-KT * (128 // group) // 4) * 4
+    assert w.codes.numel() == n * RT * KT * 1024 and w.scales.numel() == n * RT * 16 * NG
     # rows and columns past the matrix: every word of theirs is code 8, every scale 0
     nib = w.codes.cpu().numpy()
     nib = np.stack([nib & 15, nib >> 4], -1).reshape(n, RT, KT, 64, 4, 8)
@@ -105,12 +106,8 @@ def test_pack_holds_the_codes_and_scales(n, R, C, group):
         for kt in range(KT):
             out = (rt * 16 + row >= R) | (kt * 128 + col >= C)
             assert np.all(nib[:, rt, kt][:, out] == 8)
-    sc = f64(w.scales).reshape(n, RT, KT, 4, 128 // group, 4)
-    for rt in range(RT):
-        for quad in range(4):
-            for r in range(4):
-                if rt * 16 + quad * 4 + r >= R:
-                    assert not sc[:, rt, :, quad, :, r].any()
+    sc = f64(w.scales).reshape(n, RT * 16, NG)
+    assert not sc[:, R:].any() and not sc[:, :, -(-C // group):].any()
 
 
 # ---- one matrix -------------------------------------------------------------
