@@ -164,7 +164,8 @@ hipError_t launch_w4_grouped_ffn(int dtype, int64_t n_max, int64_t d, int64_t E,
                                  int64_t n_in, const int32_t* a_rows, const int32_t* offsets, const void* const* codes,
                                  const void* const* scales, void* y_perm, void* x_planes, void* h_planes,
                                  int num_cu, hipStream_t stream);
-// Token tiles that a grouped product launches for n_max rows of E experts.
+// Tiles of 16 token rows that a product launches for n_max rows of E experts (E = 0: of one
+// matrix, all n_max of them).
 int64_t w4_token_tiles(int64_t n_max, int64_t E);
 
 }  // namespace moe

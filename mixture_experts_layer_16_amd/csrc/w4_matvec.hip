@@ -29,42 +29,6 @@
 #include "tile_walk.h"
 #include "w4.h"
 
-#ifndef W4_D1
-#define W4_D1 4
-#endif
-#ifndef W4_D2
-#define W4_D2 2
-#endif
-#ifndef W4_KSD
-#define W4_KSD 4
-#endif
-#ifndef W4_KSU
-#define W4_KSU 4
-#endif
-#ifndef W4_NTD
-#define W4_NTD 2
-#endif
-#ifndef W4_NTU
-#define W4_NTU 2
-#endif
-#ifndef W4_DS
-#define W4_DS 4
-#endif
-#ifndef W4_NTM
-#define W4_NTM 2
-#endif
-#ifndef W4_NTMD
-#define W4_NTMD 2
-#endif
-#ifndef W4_SCHED
-#define W4_SCHED __builtin_amdgcn_sched_barrier(0)
-#endif
-#ifndef W4_OCC
-#define W4_OCC 3
-#endif
-#ifndef W4_FULL
-#define W4_FULL 12
-#endif
 namespace moe {
 
 namespace {
@@ -88,7 +52,7 @@ struct W4Args {
 
 struct TokenTile {
   int e;                       // expert, or -1: no such tile
-  int row0, rows;              // rows: 1 .. tok
+  int row0, rows;              // rows: 1 .. kTok
 };
 
 // Inclusive scans over the 64 lanes in registers: shifts inside each row of 16 lanes,
@@ -103,10 +67,10 @@ template <typename F> __device__ __forceinline__ int lane_scan(int v, int identi
   return v;
 }
 
-// The slot-th tile of `tok` rows over the experts' segments (tile_walk.h's bounds: the
+// The slot-th tile of 16 rows over the experts' segments (tile_walk.h's bounds: the
 // offsets are not trusted).  Every wavefront scans for itself, 64 experts a step: a
 // running maximum of the offsets and a running sum of the experts' tiles.
-__device__ __forceinline__ TokenTile find_tile(const int32_t* offsets, int E, int64_t n_max, int tok, int slot) {
+__device__ __forceinline__ TokenTile find_tile(const int32_t* offsets, int E, int64_t n_max, int slot) {
   const int lane = threadIdx.x & 63;
   int prev = offsets[0], base = 0;
   for (int e0 = 0; e0 < E; e0 += 64) {
@@ -116,15 +80,15 @@ __device__ __forceinline__ TokenTile find_tile(const int32_t* offsets, int E, in
     int below = __shfl_up(top, 1, 64);
     if (lane == 0) below = prev;
     const int hi = (int)clamp64(top, 0, n_max), lo = (int)clamp64(below, 0, n_max);
-    const int own = e < E ? (hi - lo + tok - 1) / tok : 0;
+    const int own = e < E ? (hi - lo + kTok - 1) / kTok : 0;
     const int sum = lane_scan(own, 0, [](int a, int b) { return a + b; });
     const unsigned long long past = __ballot(base + sum > slot);
     if (past != 0) {
       const int src = __ffsll(past) - 1;
       const int t = slot - base - (__builtin_amdgcn_readlane(sum, src) - __builtin_amdgcn_readlane(own, src));
-      const int row0 = __builtin_amdgcn_readlane(lo, src) + t * tok;
+      const int row0 = __builtin_amdgcn_readlane(lo, src) + t * kTok;
       const int left = __builtin_amdgcn_readlane(hi, src) - row0;
-      return {e0 + src, row0, left < tok ? left : tok};
+      return {e0 + src, row0, left < kTok ? left : kTok};
     }
     base += __builtin_amdgcn_readlane(sum, 63);
     prev = __builtin_amdgcn_readlane(top, 63);
@@ -194,14 +158,14 @@ __device__ __forceinline__ void lds_barrier() {
 // How the planes of a tile's rows are laid over MFMA rows.  Where SLOT rows of each plane
 // fit 16 together they share one MFMA (plane p of row r is MFMA row p * SLOT + r, and the
 // planes' results are added at the end); with SLOT 16 each plane has MFMAs of its own, which
-// follow one another into the same accumulators, and there may be CT tiles of 16 rows.
-template <int PLANES, int SLOT, int CT> struct Rows {
+// follow one another into the same accumulators.  (Two tiles of 16 rows a wavefront, so
+// that 17 to 32 rows unpack a weight once, measured no faster: 30.4 us against 27.7 for 96
+// rows of a 6,144 x 6,144 matrix.)
+template <int PLANES, int SLOT> struct Rows {
   static constexpr bool kPacked = PLANES * SLOT <= 16;
-  static constexpr int kMfma = kPacked ? 1 : PLANES;          // planes that follow one another
-  static constexpr int kGroups = kPacked ? PLANES * SLOT / 4 : 4 * CT;   // groups of four rows of one load unit
-  static constexpr int kTile = kMfma * CT * 4096;             // LDS bytes of 128 columns
-  static constexpr int kUnits = kMfma;                        // load units of a column tile
-  static_assert(CT == 1 || !kPacked || PLANES == 1);
+  static constexpr int kUnits = kPacked ? 1 : PLANES;         // load units of a column tile: planes that follow one another
+  static constexpr int kGroups = kPacked ? PLANES * SLOT / 4 : 4;        // groups of four rows of a load unit
+  static constexpr int kTile = kUnits * 4096;                 // LDS bytes of 128 columns
 };
 
 // Activations go through LDS: a lane's MFMA operand is 16 bytes of row lane%16, and loaded
@@ -210,12 +174,12 @@ template <int PLANES, int SLOT, int CT> struct Rows {
 // 210 us against 182 without these loads).  Instead a load takes 256 contiguous bytes of
 // each of four rows, one write puts them down and four reads pick the operands up.  Piece j
 // of row r lies at j ^ r, so that the 16 rows of a read are in 16 different bank groups.
-template <int PLANES, int SLOT, int CT> struct RowLoads {
-  using L = Rows<PLANES, SLOT, CT>;
+template <int PLANES, int SLOT> struct RowLoads {
+  using L = Rows<PLANES, SLOT>;
   static constexpr int RG = L::kGroups;
   __amdgpu_buffer_rsrc_t xr;
-  uint32_t off[RG], last[RG];        // in the last column tile, columns past the row are not there either
-  uint32_t plane;                    // bytes between planes
+  uint32_t off[RG], last[RG];                  // in the last column tile, columns past the row are not there either
+  uint32_t plane;                              // bytes between planes
   int put[RG], KT;
   __device__ __forceinline__ RowLoads(const W4Args& a, int row0, int rows) : KT(a.KT) {
     const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4;
@@ -225,12 +189,12 @@ template <int PLANES, int SLOT, int CT> struct RowLoads {
 #pragma unroll
     for (int g = 0; g < RG; ++g) {
       const int v = g * 4 + quad, r = L::kPacked ? v % SLOT : v;
-      off[g] = kNowhere;             // rows that are not there load nothing, and so zeros
+      off[g] = kNowhere;                       // rows that are not there load nothing, and so zeros
       if (r < rows)
         off[g] = (uint32_t)(a.a_rows ? clamp_row(a.a_rows[row0 + r], a.n_in) : row0 + r) * (uint32_t)(a.C * 2) +
                  col * 16 + (L::kPacked ? v / SLOT * plane : 0u);
       last[g] = cut ? kNowhere : off[g];
-      put[g] = v * 256 + ((col ^ (v & 15)) * 16);
+      put[g] = v * 256 + ((col ^ v) * 16);
     }
   }
   // unit u of column tile k, clamped to the row's
@@ -239,65 +203,50 @@ template <int PLANES, int SLOT, int CT> struct RowLoads {
 #pragma unroll
     for (int g = 0; g < RG; ++g) x[g] = load16(xr, kc == KT - 1 ? last[g] : off[g], u * plane + kc * (kW4Cols * 2));
   }
-  __device__ __forceinline__ void store(const u32x4 (&x)[RG], int u, char* tile) const {
+  __device__ __forceinline__ void store(const u32x4 (&x)[RG], char* unit) const {
 #pragma unroll
-    for (int g = 0; g < RG; ++g) *reinterpret_cast<u32x4*>(tile + u * (CT * 4096) + put[g]) = x[g];
+    for (int g = 0; g < RG; ++g) *reinterpret_cast<u32x4*>(unit + put[g]) = x[g];
   }
 };
 
 // One column tile of NT streams of weights against an LDS tile of rows.  s holds the scales
 // of the streams' groups, this tile's from group s_at on.
-template <int MP, bool FINE, int GPT, int CT, int NT>
+template <int MP, bool FINE, int GPT, int NT>
 __device__ __forceinline__ void multiply_tile(const char* tile, const u32x4 (&w)[NT], const uint2 (&s)[NT], int s_at,
-                                              bf16x8 minus, const UnpackConstants& consts, f32x4 (&total)[NT][CT]) {
+                                              bf16x8 minus, const UnpackConstants& consts, f32x4 (&total)[NT]) {
   constexpr int M = 4 / GPT;         // MFMAs of a group
   const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4;
-  bf16x8 b[CT][MP][4];
+  bf16x8 b[MP][4];
 #pragma unroll
-  for (int c = 0; c < CT; ++c)
+  for (int p = 0; p < MP; ++p)
 #pragma unroll
-    for (int p = 0; p < MP; ++p)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        b[c][p][i] = *reinterpret_cast<const bf16x8*>(tile + p * (CT * 4096) + c * 4096 + col * 256 +
-                                                      (((i * 4 + quad) ^ col) * 16));
+    for (int i = 0; i < 4; ++i)
+      b[p][i] = *reinterpret_cast<const bf16x8*>(tile + p * 4096 + col * 256 + (((i * 4 + quad) ^ col) * 16));
 #pragma unroll
   for (int g = 0; g < GPT; ++g) {
-    f32x4 c0[CT];
+    f32x4 c0 = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int c = 0; c < CT; ++c) {
-      c0[c] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int i = g * M; i < (g + 1) * M; ++i)
 #pragma unroll
-      for (int i = g * M; i < (g + 1) * M; ++i)
-#pragma unroll
-        for (int p = 0; p < MP; ++p) c0[c] = mfma(b[c][p][i], minus, c0[c]);
-    }
+      for (int p = 0; p < MP; ++p) c0 = mfma(b[p][i], minus, c0);
 #pragma unroll
     for (int m = 0; m < NT; ++m) {
-      f32x4 acc[CT];
-#pragma unroll
-      for (int c = 0; c < CT; ++c) acc[c] = c0[c];
+      f32x4 acc = c0;
 #pragma unroll
       for (int i = g * M; i < (g + 1) * M; ++i) {
         const bf16x8 wf = unpack<FINE>(w[m][i], consts);
 #pragma unroll
-        for (int c = 0; c < CT; ++c)
-#pragma unroll
-          for (int p = 0; p < MP; ++p) acc[c] = mfma(b[c][p][i], wf, acc[c]);
+        for (int p = 0; p < MP; ++p) acc = mfma(b[p][i], wf, acc);
       }
       const float sc = scale_at(s[m], s_at + g);
 #pragma unroll
-      for (int c = 0; c < CT; ++c)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) total[m][c][i] = fmaf(sc, acc[c][i], total[m][c][i]);
+      for (int i = 0; i < 4; ++i) total[m][i] = fmaf(sc, acc[i], total[m][i]);
     }
   }
   // the sums are due here: moved behind the loop's other tiles they would keep every
   // group's accumulators alive
 #pragma unroll
-  for (int m = 0; m < NT; ++m)
-#pragma unroll
-    for (int c = 0; c < CT; ++c) asm volatile("" : "+v"(total[m][c]));
+  for (int m = 0; m < NT; ++m) asm volatile("" : "+v"(total[m]));
 }
 
 // The buffers of one set of NT streams.  SWIGLU: row tiles of the gate and up matrices in
@@ -340,13 +289,13 @@ template <int NT, int GPT, bool SWIGLU> struct Streams {
 // unit of the next kWaves for all: a quarter of the loads, and one barrier for them (it waits
 // for LDS only, the weights stay in flight).  Otherwise a wavefront has columns and LDS of
 // its own.
-template <int PLANES, int SLOT, int CT, int GPT, int NT, int DEPTH, bool SHARED, bool SWIGLU>
+template <int PLANES, int SLOT, int GPT, int NT, int DEPTH, bool SHARED, bool SWIGLU>
 __device__ __forceinline__ void stream(const W4Args& a, const Streams<NT, GPT, SWIGLU>& from, int k0, int row0, int rows,
-                                       char* lds, f32x4 (&total)[NT][CT]) {
-  using L = Rows<PLANES, SLOT, CT>;
+                                       char* lds, f32x4 (&total)[NT]) {
+  using L = Rows<PLANES, SLOT>;
   constexpr bool FINE = PLANES == 3;
   constexpr int SB = 4 / GPT < DEPTH ? 4 / GPT : DEPTH;       // column tiles of a scale load
-  const RowLoads<PLANES, SLOT, CT> rl(a, row0, rows);
+  const RowLoads<PLANES, SLOT> rl(a, row0, rows);
   const bf16x8 minus = offset_operand<FINE>();
   const UnpackConstants consts;
   u32x4 w[DEPTH][NT];
@@ -358,7 +307,7 @@ __device__ __forceinline__ void stream(const W4Args& a, const Streams<NT, GPT, S
     const int tile = wave / L::kUnits, unit = wave % L::kUnits;
     u32x4 x[L::kGroups];
     auto put = [&](int half) {
-      if (tile < CH) rl.store(x, unit, lds + (half * CH + tile) * L::kTile);
+      if (tile < CH) rl.store(x, lds + (half * CH + tile) * L::kTile + unit * 4096);
       lds_barrier();
     };
     rl.load(x, unit, tile);
@@ -374,21 +323,24 @@ __device__ __forceinline__ void stream(const W4Args& a, const Streams<NT, GPT, S
       for (int v = 0; v < U; ++v) {
         const int u = v % DEPTH;
         if (v % CH == 0) rl.load(x, unit, k + v + CH + tile);
-        multiply_tile<L::kMfma, FINE, GPT, CT, NT>(lds + (half * CH + v % CH) * L::kTile, w[u], s[u / SB],
-                                                   u % SB * GPT, minus, consts, total);
+        multiply_tile<L::kUnits, FINE, GPT, NT>(lds + (half * CH + v % CH) * L::kTile, w[u], s[u / SB], u % SB * GPT,
+                                                minus, consts, total);
         from.load(w[u], k + v + DEPTH);
         if (u % SB == SB - 1) from.template load_scales_of<SB>(s[u / SB], k + v + 1 - SB + DEPTH);
         if (v % CH == CH - 1) put(half ^= 1);  // the other half was last read before the last barrier
-        W4_SCHED;
+        __builtin_amdgcn_sched_barrier(0);     // tiles interleaved by the scheduler need the registers of a whole turn
       }
     }
   } else {
     u32x4 x[DEPTH][L::kUnits][L::kGroups];
+    auto load_x = [&](int u, int k) {
+#pragma unroll
+      for (int q = 0; q < L::kUnits; ++q) rl.load(x[u][q], q, k);
+    };
 #pragma unroll
     for (int u = 0; u < DEPTH; ++u) {
       from.load(w[u], u);
-#pragma unroll
-      for (int p = 0; p < L::kUnits; ++p) rl.load(x[u][p], p, k0 + u);
+      load_x(u, k0 + u);
       if (u % SB == 0) from.template load_scales_of<SB>(s[u / SB], u);
     }
     for (int k = 0; k < from.n; k += DEPTH) {
@@ -396,14 +348,13 @@ __device__ __forceinline__ void stream(const W4Args& a, const Streams<NT, GPT, S
       for (int u = 0; u < DEPTH; ++u) {
         lds_order();                           // the operands before these have been read
 #pragma unroll
-        for (int p = 0; p < L::kUnits; ++p) rl.store(x[u][p], p, lds);
+        for (int q = 0; q < L::kUnits; ++q) rl.store(x[u][q], lds + q * 4096);
         lds_order();
-        multiply_tile<L::kMfma, FINE, GPT, CT, NT>(lds, w[u], s[u / SB], u % SB * GPT, minus, consts, total);
+        multiply_tile<L::kUnits, FINE, GPT, NT>(lds, w[u], s[u / SB], u % SB * GPT, minus, consts, total);
         from.load(w[u], k + u + DEPTH);
-#pragma unroll
-        for (int p = 0; p < L::kUnits; ++p) rl.load(x[u][p], p, k0 + k + u + DEPTH);
+        load_x(u, k0 + k + u + DEPTH);
         if (u % SB == SB - 1) from.template load_scales_of<SB>(s[u / SB], k + u + 1 - SB + DEPTH);
-        W4_SCHED;
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
   }
@@ -414,10 +365,10 @@ __device__ __forceinline__ void stream(const W4Args& a, const Streams<NT, GPT, S
     for (int m = 0; m < NT; ++m)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        float v = quad * 4 < PLANES * SLOT ? total[m][0][i] : 0.f;
+        float v = quad * 4 < PLANES * SLOT ? total[m][i] : 0.f;
         if (SLOT == 4) v += __shfl_xor(v, 16, 64);
         if (PLANES * SLOT > 8) v += __shfl_xor(v, 32, 64);
-        total[m][0][i] = v;
+        total[m][i] = v;
       }
   }
 }
@@ -451,27 +402,26 @@ __device__ __forceinline__ void store_results(const W4Args& a, const f32x4 (&v)[
   }
 }
 
-// Up to CT * 16 token rows a workgroup (blockIdx.y) and some of the weight rows: KS
-// wavefronts share a set of NT streams, each a run of their column tiles.
-template <int PLANES, int GPT, int CT, int KS, int NT, int DEPTH, bool SWIGLU, int OUT, typename TO>
-__global__ __launch_bounds__(64 * kWaves, W4_OCC) void w4_matvec_kernel(W4Args a) {
-  constexpr int kRows = SWIGLU ? NT / 2 : NT;                 // row tiles of a set
+// Up to 16 token rows a workgroup (blockIdx.y) and some of the weight rows: KS wavefronts
+// share a set of NT streams, each a run of their column tiles.
+template <int PLANES, int GPT, int KS, int NT, bool SWIGLU, int OUT, typename TO>
+__global__ __launch_bounds__(64 * kWaves, 3) void w4_matvec_kernel(W4Args a) {
   constexpr bool kShared = KS == 1;
-  // LDS: two chunks of column tiles, or one column tile a wavefront
-  constexpr int kTile = Rows<PLANES, 16, CT>::kTile, kPack = 4096 * CT;
-  constexpr int kLds = kShared ? 2 * (kWaves / PLANES * kTile > kWaves * kPack ? kWaves / PLANES * kTile : kWaves * kPack)
-                               : kWaves * kTile;
-  constexpr int kRed = KS > 1 ? kWaves * NT * CT * 1024 : 0;
+  constexpr int DEPTH = kShared || PLANES == 1 ? 4 : 2;       // private activations take registers ahead of time too
+  constexpr int kRows = SWIGLU ? NT / 2 : NT;                 // row tiles of a set
+  // LDS: two chunks of column tiles (at most kWaves load units each), or a column tile a wavefront
+  constexpr int kTile = Rows<PLANES, 16>::kTile, kLds = (kShared ? 2 : PLANES) * kWaves * 4096;
+  constexpr int kRed = KS > 1 ? kWaves * NT * 1024 : 0;
   __shared__ __attribute__((aligned(16))) char lds[kLds > kRed ? kLds : kRed];
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), lane = threadIdx.x & 63;
 
   TokenTile tt;
   if (a.offsets) {
-    tt = find_tile(a.offsets, a.E, a.n_max, CT * kTok, (int)blockIdx.y);
+    tt = find_tile(a.offsets, a.E, a.n_max, (int)blockIdx.y);
     if (tt.e < 0) return;
   } else {
-    const int64_t r0 = (int64_t)blockIdx.y * (CT * kTok), left = a.n_max - r0;
-    tt = {0, (int)r0, left < CT * kTok ? (int)left : CT * kTok};
+    const int r0 = (int)blockIdx.y * kTok, left = (int)a.n_max - r0;
+    tt = {0, r0, left < kTok ? left : kTok};
   }
   const int64_t e = __builtin_amdgcn_readfirstlane(tt.e);
   const int row0 = __builtin_amdgcn_readfirstlane(tt.row0), rows = __builtin_amdgcn_readfirstlane(tt.rows);
@@ -481,48 +431,31 @@ __global__ __launch_bounds__(64 * kWaves, W4_OCC) void w4_matvec_kernel(W4Args a
   constexpr int SB = 4 / GPT < DEPTH ? 4 / GPT : DEPTH;
   const int run = ((a.KT + KS - 1) / KS + SB - 1) / SB * SB, k0 = (wave % KS) * run;
   const int n = (!kShared && first >= a.RT) || k0 >= a.KT ? 0 : (a.KT - k0 < run ? a.KT - k0 : run);
-  f32x4 total[NT][CT];
+  f32x4 total[NT];
 #pragma unroll
-  for (int m = 0; m < NT; ++m)
-#pragma unroll
-    for (int c = 0; c < CT; ++c) total[m][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int m = 0; m < NT; ++m) total[m] = f32x4{0.f, 0.f, 0.f, 0.f};
   if (n > 0) {
     const Streams<NT, GPT, SWIGLU> from(a, e, first, k0, n);
     char* mine = kShared ? lds : lds + wave * kTile;
-    if (CT == 1 && rows <= 4)
-      stream<PLANES, CT == 1 ? 4 : 16, CT, GPT, NT, DEPTH, kShared>(a, from, k0, row0, rows, mine, total);
-    else if (CT == 1 && PLANES < 3 && rows <= 8)
-      stream<PLANES, CT == 1 && PLANES < 3 ? 8 : 16, CT, GPT, NT, DEPTH, kShared>(a, from, k0, row0, rows, mine, total);
-    else
-      stream<PLANES, 16, CT, GPT, NT, DEPTH, kShared>(a, from, k0, row0, rows, mine, total);
+    constexpr int kSlot8 = PLANES < 3 ? 8 : 16;
+    if (rows <= 4) stream<PLANES, 4, GPT, NT, DEPTH, kShared>(a, from, k0, row0, rows, mine, total);
+    else if (rows <= kSlot8) stream<PLANES, kSlot8, GPT, NT, DEPTH, kShared>(a, from, k0, row0, rows, mine, total);
+    else stream<PLANES, 16, GPT, NT, DEPTH, kShared>(a, from, k0, row0, rows, mine, total);
   }
 
-  f32x4* red = reinterpret_cast<f32x4*>(lds);                 // [wave][NT][CT][lane]
   if constexpr (KS > 1) {
+    f32x4* red = reinterpret_cast<f32x4*>(lds);               // [wave][NT][lane]
     __syncthreads();
 #pragma unroll
-    for (int m = 0; m < NT; ++m)
-#pragma unroll
-      for (int c = 0; c < CT; ++c) red[((wave * NT + m) * CT + c) * 64 + lane] = total[m][c];
+    for (int m = 0; m < NT; ++m) red[(wave * NT + m) * 64 + lane] = total[m];
     __syncthreads();
+    if (wave % KS != 0) return;
+#pragma unroll
+    for (int q = 1; q < KS; ++q)
+#pragma unroll
+      for (int m = 0; m < NT; ++m) total[m] += red[((wave + q) * NT + m) * 64 + lane];
   }
-  if (first >= a.RT) return;
-#pragma unroll
-  for (int c = 0; c < CT; ++c) {
-    if (KS > 1 && c % KS != wave % KS) continue;
-    f32x4 v[NT];
-#pragma unroll
-    for (int m = 0; m < NT; ++m) {
-      v[m] = total[m][c];
-      if constexpr (KS > 1) {
-        const int w0 = wave - wave % KS;
-        v[m] = red[((w0 * NT + m) * CT + c) * 64 + lane];
-#pragma unroll
-        for (int q = 1; q < KS; ++q) v[m] += red[(((w0 + q) * NT + m) * CT + c) * 64 + lane];
-      }
-    }
-    store_results<NT, SWIGLU, OUT, TO>(a, v, first, row0 + c * kTok, rows - c * kTok);
-  }
+  if (first < a.RT) store_results<NT, SWIGLU, OUT, TO>(a, total, first, row0, rows);
 }
 
 // float32 x as three bf16 planes that sum to it (24 bits)
@@ -542,22 +475,30 @@ __global__ __launch_bounds__(256) void split3_kernel(int64_t n, const float* __r
   }
 }
 
-template <int PLANES, int GPT, int CT, int KS, int NT, bool SWIGLU, int OUT, typename TO>
+template <int PLANES, int GPT, int KS, int NT, bool SWIGLU, int OUT, typename TO>
 void launch_one(const W4Args& a, hipStream_t stream, int64_t token_tiles) {
-  constexpr int DEPTH = KS == 1 ? 4 : PLANES == 1 ? W4_D1 : W4_D2;
   const int per = kWaves / KS * (SWIGLU ? NT / 2 : NT);       // row tiles of a workgroup
-  hipLaunchKernelGGL((w4_matvec_kernel<PLANES, GPT, CT, KS, NT, DEPTH, SWIGLU, OUT, TO>),
+  hipLaunchKernelGGL((w4_matvec_kernel<PLANES, GPT, KS, NT, SWIGLU, OUT, TO>),
                      dim3((unsigned)((a.RT + per - 1) / per), (unsigned)token_tiles), dim3(64 * kWaves), 0, stream, a);
 }
 
+// How many wavefronts share the columns: as few as still fill the card, since longer runs
+// lose less to their start and end.  A CU holds 12 wavefronts; measured (bf16, columns
+// 6,144 and 1,792, 96 experts): one token, 7 and 6 wavefronts a CU at KS 2, 32.7 us (36.2 at
+// KS 4, 36.4 with the down product at KS 1); two tokens, 7 at KS 1, 53.6 us (56.0 at KS 2).
+// Fuller tiles, whose activations cost more, gain earlier from sharing them: 16 rows of 8
+// experts (4,096 and 1,536) with 3 at KS 1 33.4 us, 39.5 at KS 2.  One matrix and one
+// token, 6,144 x 6,144: a stream of its own for each of four wavefronts 6.8 us, two 7.7.
 template <int PLANES, int GPT, bool SWIGLU, int OUT, typename TO>
 void launch_group(const W4Args& a, int num_cu, hipStream_t stream) {
-  const int64_t tiles = a.offsets ? w4_token_tiles(a.n_max, a.E) : (a.n_max + kTok - 1) / kTok;
-  const int64_t busy = a.offsets ? (a.n_max < a.E ? a.n_max : a.E) : tiles;    // tiles with rows, about
-  const int64_t waves = a.RT / (SWIGLU ? 2 : 4) * busy;
-  if (waves >= (int64_t)num_cu * W4_FULL)
-    launch_one<PLANES, GPT, 1, 1, SWIGLU ? W4_NTM : W4_NTMD, SWIGLU, OUT, TO>(a, stream, tiles);
-  else launch_one<PLANES, GPT, 1, SWIGLU ? W4_KSU : W4_KSD, SWIGLU ? W4_NTU : W4_NTD, SWIGLU, OUT, TO>(a, stream, tiles);
+  const int64_t tiles = w4_token_tiles(a.n_max, a.offsets ? a.E : 0);
+  const int64_t used = a.n_max < a.E ? a.n_max : a.E, most = a.n_max / kTok;
+  const int64_t busy = used > most ? used : most;             // token tiles with rows, about
+  const int64_t waves = (SWIGLU ? a.RT : (a.RT + 1) / 2) * busy, enough = a.n_max >= 8 * busy ? 3 : 7;
+  if (waves >= num_cu * enough) launch_one<PLANES, GPT, 1, 2, SWIGLU, OUT, TO>(a, stream, tiles);
+  else if (waves >= num_cu * 3) launch_one<PLANES, GPT, 2, 2, SWIGLU, OUT, TO>(a, stream, tiles);
+  else if (SWIGLU || waves * 2 >= num_cu * 3) launch_one<PLANES, GPT, 4, 2, SWIGLU, OUT, TO>(a, stream, tiles);
+  else launch_one<PLANES, GPT, 4, SWIGLU ? 2 : 1, SWIGLU, OUT, TO>(a, stream, tiles);
 }
 
 template <int PLANES, bool SWIGLU, int OUT, typename TO>
@@ -578,7 +519,7 @@ hipError_t launch_split3(int64_t n, const void* x, void* planes, hipStream_t str
 
 int64_t w4_token_tiles(int64_t n_max, int64_t E) {
   // each expert with rows has one last, perhaps partial tile
-  return n_max / kTok + (n_max < E ? n_max : E);
+  return E == 0 ? (n_max + kTok - 1) / kTok : n_max / kTok + (n_max < E ? n_max : E);
 }
 
 hipError_t launch_w4_matvec(int dtype, int64_t T, int64_t C, int64_t R, int group, const void* x, const void* codes,
