@@ -466,8 +466,9 @@ moe_status moe_block_norm_backward(int64_t T, int64_t d, moe_dtype dtype, const 
 
 /*
  * moe_w4_quantize: 4-bit codes and scales of n matrices w [n,R,C] in dtype:
- *   s = bf16(max over the group of |w| / 7),  q = 8 + round(w / s) clamped to 0..15
- * (halves to even; a group whose s is 0 has q = 8).
+ *   s = bf16(max over the group of |w| * (1/7 in float32)),
+ *   q = 8 + round(w / s) clamped to 0..15
+ * (the product rounded to float32 first, halves to even; a group whose s is 0 has q = 8).
  * moe_w4_pack: the same layout from codes and scales that are already there:
  *   q [n,R,C/2] bytes (even column in the low four bits), s [n,R,ceil(C/group)] bf16.
  * moe_w4_dequantize: w [n,R,C] in dtype = s * (q - 8), rounded once.

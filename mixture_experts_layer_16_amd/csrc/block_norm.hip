@@ -9,10 +9,11 @@
 // expert rows, taken here without a pass of its own through memory.  Without y,
 // out = x: the norm before a first block.
 //
-// A row lives in the registers of one team (a wavefront for d <= 1,024, a workgroup
-// above), so every tensor is read once and written once; all that crosses lanes are
-// the row sums.  What bounds the kernels is memory, and for a few rows the latency of
-// one load, two row sums and one store.
+// A row lives in the registers of one team: eight of its elements a lane (sixteen above
+// 8,192), so a team is as many wavefronts as the row needs.  Teams walk over rows with the
+// gains in registers and the next row's loads in flight; every tensor is read once and
+// written once, and all that crosses lanes are the row sums.  What bounds the kernels is
+// memory, and for a few rows the latency of one load, two row sums and one store.
 #include "common.h"
 #include "kernels.h"
 #include "rows.h"
@@ -35,9 +36,10 @@ __device__ __forceinline__ float gate_slope(float a, int act) {
   return 1.f;
 }
 
-// Sums of NS values over a team of TEAM threads; every thread ends with the same bits.
-// Two buffers in turn: a wavefront writes a buffer again only after the barrier of the
-// sum in between, which all others reach after reading it.
+// Sums of NS values over a team of TEAM threads (a workgroup, where it is more than one
+// wavefront); every thread ends with the same bits.  Two buffers in turn: a wavefront
+// writes a buffer again only after the barrier of the sum in between, which all others
+// reach after reading it.
 template <int TEAM, int NS> struct TeamSum {
   float (*buf)[NS][TEAM / 64];
   int turn = 0;
@@ -50,7 +52,7 @@ template <int TEAM, int NS> struct TeamSum {
 #pragma unroll
         for (int s = 0; s < NS; ++s) buf[turn][s][wave] = v[s];
       }
-      __syncthreads();
+      lds_barrier();
 #pragma unroll
       for (int s = 0; s < NS; ++s) {
         v[s] = buf[turn][s][0];
@@ -62,95 +64,152 @@ template <int TEAM, int NS> struct TeamSum {
   }
 };
 
-template <typename T, int TEAM, int NV>
-__global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void block_norm_kernel(BlockNormArgs a) {
-  constexpr int kTeams = TEAM < 256 ? 256 / TEAM : 1;
-  __shared__ float buf[2][1][TEAM / 64];
-  TeamSum<TEAM, 1> sum{buf};
-  const int lane = threadIdx.x % TEAM;
-  const int team = __builtin_amdgcn_readfirstlane((int)blockIdx.x * kTeams + (TEAM < 256 ? (int)threadIdx.x / TEAM : 0));
-  const int n8 = a.d / 8;
-  const float inv_d = 1.f / (float)a.d;
-  const T* x = static_cast<const T*>(a.x);
-  for (int64_t t = team; t < a.T; t += (int64_t)gridDim.x * kTeams) {
-    const int64_t base = t * a.d;
-    float out[NV][8], y[NV][8];
+constexpr int block_threads(int team) { return team < 256 && team == 64 ? 256 : team; }
+
+// This lane's pieces of a row: piece i is elements (i * TEAM + lane) * 8 .. + 7.
+template <int TEAM, int NV> struct Pieces {
+  int col[NV];
+  bool in[NV];
+  __device__ __forceinline__ explicit Pieces(int d) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = i * TEAM + lane;
-      if (c < n8) load8(x + base + c * 8, out[i]);
-      else
-#pragma unroll
-        for (int j = 0; j < 8; ++j) out[i][j] = 0.f;
+      col[i] = (i * TEAM + (int)threadIdx.x % TEAM) * 8;
+      in[i] = col[i] < d;
     }
+  }
+  template <bool NT, typename T> __device__ __forceinline__ void load(Row8<T> (&v)[NV], const T* row) const {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (in[i]) load_row8<NT>(v[i], row + col[i]);
+  }
+  __device__ __forceinline__ void gains(float (&v)[NV][8], const float* g) const {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (in[i]) load8(g + col[i], v[i]);
+  }
+};
+
+// The gate's values (and slopes) for the row's group, computed again only where the group changes.
+template <typename T, int TEAM, int NV, bool SLOPE> struct Gate {
+  float a[NV][8], slope[SLOPE ? NV : 1][8];
+  int64_t group = -1;
+  __device__ __forceinline__ void at(const Pieces<TEAM, NV>& p, const void* gate, int64_t g, int d, int act) {
+    if (g == group) return;
+    group = g;
+    Row8<T> z[NV] = {};
+    p.template load<false>(z, static_cast<const T*>(gate) + g * d);
+    from(z, act);
+  }
+  __device__ __forceinline__ void from(const Row8<T> (&z)[NV], int act) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        a[i][j] = gate_act(z[i].get(j), act);
+        if constexpr (SLOPE) slope[i][j] = gate_slope(a[i][j], act);
+        __builtin_amdgcn_sched_barrier(0);     // one function at a time: eight side by side are what needs the most registers
+      }
+    }
+  }
+};
+
+// NT: rows go past the caches.  COMBINE: y is summed from expert rows.  TOKEN: the gate has a
+// row a token (otherwise none, or one for several).
+template <typename T, int TEAM, int NV, bool NT, bool COMBINE, bool TOKEN>
+__global__ __launch_bounds__(block_threads(TEAM)) void block_norm_kernel(BlockNormArgs a) {
+  constexpr int kTeams = block_threads(TEAM) / TEAM;
+  __shared__ float buf[2][1][TEAM / 64];
+  TeamSum<TEAM, 1> sum{buf};
+  const int team = __builtin_amdgcn_readfirstlane((int)blockIdx.x * kTeams + (kTeams > 1 ? (int)threadIdx.x / TEAM : 0));
+  const int64_t step = (int64_t)gridDim.x * kTeams;
+  const Pieces<TEAM, NV> p(a.d);
+  const float inv_d = 1.f / (float)a.d;
+  const T* xs = static_cast<const T*>(a.x);
+  const T* ys = static_cast<const T*>(a.y);
+  const T* zs = static_cast<const T*>(a.gate);
+  Row8<T> x[NV], y[NV], z[NV], x_next[NV], y_next[NV], z_next[NV];
+  if (team < a.T) {
+    p.template load<NT>(x, xs + (int64_t)team * a.d);
+    if (!COMBINE && ys) p.template load<NT>(y, ys + (int64_t)team * a.d);
+    if (TOKEN) p.template load<NT>(z, zs + (int64_t)team * a.d);
+  }
+  float g1[NV][8], g2[NV][8];
+  if (a.post_gain) p.gains(g1, a.post_gain);
+  if (a.next_gain) p.gains(g2, a.next_gain);
+  Gate<T, TEAM, NV, false> gate;
+  for (int64_t t = team; t < a.T; t += step) {
+    const int64_t base = t * a.d;
+    if (t + step < a.T) {
+      p.template load<NT>(x_next, xs + base + step * a.d);
+      if (!COMBINE && ys) p.template load<NT>(y_next, ys + base + step * a.d);
+      if (TOKEN) p.template load<NT>(z_next, zs + base + step * a.d);
+    }
+    float out[NV][8];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) out[i][j] = p.in[i] ? x[i].get(j) : 0.f;
     if (a.has_y) {
-      if (a.y) {
-        const T* yp = static_cast<const T*>(a.y);
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          const int c = i * TEAM + lane;
-          if (c < n8) load8(yp + base + c * 8, y[i]);
-          else
-#pragma unroll
-            for (int j = 0; j < 8; ++j) y[i][j] = 0.f;
-        }
-      } else {
+      float v[NV][8];
+      if constexpr (COMBINE) {
         const T* yp = static_cast<const T*>(a.y_perm);
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) y[i][j] = 0.f;
-        for (int s = 0; s < a.k; ++s) {
-          const int row = __builtin_amdgcn_readfirstlane(a.slot_row[t * a.k + s]);
-          if ((unsigned)row >= (unsigned)a.n_rows) continue;
-          const float w = a.topk_w[t * a.k + s];
+          for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+        for (int s0 = 0; s0 < a.k; s0 += 4) {  // four expert rows in flight (eight: the same time)
+          Row8<T> e[4][NV];
+          float w[4];
 #pragma unroll
-          for (int i = 0; i < NV; ++i) {
-            const int c = i * TEAM + lane;
-            if (c >= n8) continue;
-            float v[8];
-            load8(yp + (int64_t)row * a.d + c * 8, v);
+          for (int s = 0; s < 4; ++s) {
+            const int row = s0 + s < a.k ? __builtin_amdgcn_readfirstlane(a.slot_row[t * a.k + s0 + s]) : -1;
+            const bool there = (unsigned)row < (unsigned)a.n_rows;
+            w[s] = there ? a.topk_w[t * a.k + s0 + s] : 0.f;
+            if (there) p.template load<NT>(e[s], yp + (int64_t)row * a.d);
+            else
 #pragma unroll
-            for (int j = 0; j < 8; ++j) y[i][j] = fmaf(w, v[j], y[i][j]);
+              for (int i = 0; i < NV; ++i) e[s][i] = {};
           }
-        }
-        if (a.y_out) {
-          T* yo = static_cast<T*>(a.y_out);
 #pragma unroll
-          for (int i = 0; i < NV; ++i) {
-            const int c = i * TEAM + lane;
-            if (c < n8) store8(yo + base + c * 8, y[i]);
-          }
+          for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+              for (int j = 0; j < 8; ++j) v[i][j] = fmaf(w[s], p.in[i] ? e[s][i].get(j) : 0.f, v[i][j]);
         }
+        if (a.y_out)
+#pragma unroll
+          for (int i = 0; i < NV; ++i)
+            if (p.in[i]) store_row8<NT>(static_cast<T*>(a.y_out) + base + p.col[i], v[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[i][j] = p.in[i] ? y[i].get(j) : 0.f;
       }
-      float r = 1.f;
+      float r = a.branch_scale;
       if (a.post_gain) {
         float ss = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) ss = fmaf(y[i][j], y[i][j], ss);
+          for (int j = 0; j < 8; ++j) ss = fmaf(v[i][j], v[i][j], ss);
         sum(&ss);
-        r = rsqrtf(ss * inv_d + a.eps);
+        r *= rsqrtf(ss * inv_d + a.eps);
       }
-      r *= a.branch_scale;
-      const T* gate = a.gate ? static_cast<const T*>(a.gate) + (t / a.gate_rows) * (int64_t)a.d : nullptr;
-      T* o = static_cast<T*>(a.out);
+      if constexpr (TOKEN) gate.from(z, a.gate_act);
+      else if (a.gate) gate.at(p, a.gate, (int64_t)((uint64_t)t / (uint64_t)a.gate_rows), a.d, a.gate_act);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int c = i * TEAM + lane;
-        if (c >= n8) continue;
-        float g[8], z[8];
-        if (a.post_gain) load8(a.post_gain + c * 8, g);
-        if (gate) load8(gate + c * 8, z);
+        if (!p.in[i]) continue;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          float v = y[i][j] * r;
-          if (a.post_gain) v *= g[j];
-          if (gate) v *= gate_act(z[j], a.gate_act);
-          out[i][j] = fmaf(a.res_scale, out[i][j], v);
+          float n = v[i][j] * r;
+          if (a.post_gain) n *= g1[i][j];
+          if (a.gate) n *= gate.a[i][j];
+          out[i][j] = fmaf(a.res_scale, out[i][j], n);
         }
-        store8(o + base + c * 8, out[i]);
+        store_row8<NT>(static_cast<T*>(a.out) + base + p.col[i], out[i]);
       }
     }
     if (a.next_gain) {
@@ -161,17 +220,19 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void block_norm_kernel(Blo
         for (int j = 0; j < 8; ++j) ss = fmaf(out[i][j], out[i][j], ss);
       sum(&ss);
       const float r = rsqrtf(ss * inv_d + a.eps);
-      T* h = static_cast<T*>(a.h);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int c = i * TEAM + lane;
-        if (c >= n8) continue;
-        float g[8];
-        load8(a.next_gain + c * 8, g);
+        if (!p.in[i]) continue;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) out[i][j] *= r * g[j];
-        store8(h + base + c * 8, out[i]);
+        for (int j = 0; j < 8; ++j) out[i][j] *= r * g2[i][j];
+        store_row8<NT>(static_cast<T*>(a.h) + base + p.col[i], out[i]);
       }
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      x[i] = x_next[i];
+      if constexpr (!COMBINE) y[i] = y_next[i];
+      if constexpr (TOKEN) z[i] = z_next[i];
     }
   }
 }
@@ -191,15 +252,15 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void block_norm_kernel(Blo
 // A team walks consecutive rows and keeps the column sums in registers; they go out once
 // at its end, and a second kernel adds the teams' parts in order (no atomics).  Rows are
 // dealt so that a team's rows either cover whole gate groups or lie in one (RowPlan).
-template <typename T, int TEAM, int NV>
-__global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void block_norm_backward_kernel(BlockNormBackwardArgs a) {
-  constexpr int kTeams = TEAM < 256 ? 256 / TEAM : 1;
+template <typename T, int TEAM, int NV, bool NT, bool TOKEN>
+__global__ __launch_bounds__(block_threads(TEAM)) void block_norm_backward_kernel(BlockNormBackwardArgs a) {
+  constexpr int kTeams = block_threads(TEAM) / TEAM;
+  constexpr bool kAhead = TEAM * NV * sizeof(T) < 2048;       // the next row fits in registers too
   __shared__ float buf[2][6][TEAM / 64];
   TeamSum<TEAM, 6> sum{buf};
-  const int lane = threadIdx.x % TEAM;
-  const int team = __builtin_amdgcn_readfirstlane((int)blockIdx.x * kTeams + (TEAM < 256 ? (int)threadIdx.x / TEAM : 0));
+  const int team = __builtin_amdgcn_readfirstlane((int)blockIdx.x * kTeams + (kTeams > 1 ? (int)threadIdx.x / TEAM : 0));
   if (team >= a.plan.teams) return;
-  int64_t lo, hi, group_end = 0;
+  int64_t lo, hi;
   const int64_t period = a.gate_rows;
   if (a.plan.teams_per_group == 0) {
     lo = (int64_t)team * a.plan.rows;
@@ -211,124 +272,116 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void block_norm_backward_k
     if (hi > (g + 1) * period) hi = (g + 1) * period;
   }
   if (hi > a.T) hi = a.T;
-  const int n8 = a.d / 8;
+  const Pieces<TEAM, NV> p(a.d);
   const float inv_d = 1.f / (float)a.d;
-  const bool sums_gate = a.gate && period > 1;
-  float acc_post[NV][8], acc_next[NV][8], acc_gate[NV][8];
+  const bool sums_gate = !TOKEN && a.gate;
+  struct Row {
+    Row8<T> o[NV], dh[NV], dout[NV], y[NV], z[TOKEN ? NV : 1];
+  };
+  auto load = [&](Row& q, int64_t t) {
+    if (a.next_gain) {
+      p.template load<NT>(q.o, static_cast<const T*>(a.out) + t * a.d);
+      p.template load<NT>(q.dh, static_cast<const T*>(a.dh) + t * a.d);
+    }
+    if (a.d_out) p.template load<NT>(q.dout, static_cast<const T*>(a.d_out) + t * a.d);
+    if (a.y) p.template load<NT>(q.y, static_cast<const T*>(a.y) + t * a.d);
+    if constexpr (TOKEN) p.template load<NT>(q.z, static_cast<const T*>(a.gate) + t * a.d);
+  };
+  // What is absent is computed with as zeros (a gain or gate as ones): branches inside the
+  // row cost more registers than the arithmetic costs time.
+  Row q{}, next{};
+  if (lo < hi) load(q, lo);
+  float g1[NV][8], g2[NV][8], acc_post[NV][8], acc_next[NV][8], acc_gate[NV][8];
+  Gate<T, TEAM, NV, true> gate;
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) acc_post[i][j] = acc_next[i][j] = acc_gate[i][j] = 0.f;
+    for (int j = 0; j < 8; ++j) {
+      acc_post[i][j] = acc_next[i][j] = acc_gate[i][j] = g2[i][j] = gate.slope[i][j] = 0.f;
+      g1[i][j] = gate.a[i][j] = 1.f;
+    }
+  const bool post = a.post_gain != nullptr, norm_next = a.next_gain != nullptr;
+  if (post) p.gains(g1, a.post_gain);
+  if (norm_next) p.gains(g2, a.next_gain);
 
   for (int64_t t = lo; t < hi; ++t) {
+    if (kAhead && t + 1 < hi) load(next, t + 1);
     const int64_t base = t * a.d;
-    typename Raw16<T>::type o[NV], dh[NV], dout[NV], y[NV], z[NV];
-    const int64_t group = a.gate ? t / period : 0;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = i * TEAM + lane;
-      if (c >= n8) continue;
-      if (a.next_gain) {
-        o[i] = Raw16<T>::load(static_cast<const T*>(a.out) + base + c * 8);
-        dh[i] = Raw16<T>::load(static_cast<const T*>(a.dh) + base + c * 8);
-      }
-      if (a.d_out) dout[i] = Raw16<T>::load(static_cast<const T*>(a.d_out) + base + c * 8);
-      if (a.y) y[i] = Raw16<T>::load(static_cast<const T*>(a.y) + base + c * 8);
-      if (a.gate) z[i] = Raw16<T>::load(static_cast<const T*>(a.gate) + group * a.d + c * 8);
-    }
+    if constexpr (TOKEN) gate.from(q.z, a.gate_act);
+    else if (a.gate) gate.at(p, a.gate, (int64_t)((uint64_t)t / (uint64_t)period), a.d, a.gate_act);
     float s[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};   // o^2, dh g2 o, y^2, c d_out, c dh g2, c o
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = i * TEAM + lane;
-      if (c >= n8) continue;
-      float g1[8], g2[8];
-      if (a.post_gain) load8(a.post_gain + c * 8, g1);
-      if (a.next_gain) load8(a.next_gain + c * 8, g2);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float ov = a.next_gain ? Raw16<T>::get(o[i], j) : 0.f;
-        const float u = a.next_gain ? Raw16<T>::get(dh[i], j) * g2[j] : 0.f;
+        const float ov = q.o[i].get(j), u = q.dh[i].get(j) * g2[i][j], yv = q.y[i].get(j);
+        const float cv = a.branch_scale * g1[i][j] * gate.a[i][j] * yv;
         s[0] = fmaf(ov, ov, s[0]);
         s[1] = fmaf(u, ov, s[1]);
-        if (a.post_gain) {
-          const float yv = Raw16<T>::get(y[i], j);
-          float cv = a.branch_scale * g1[j] * yv;
-          if (a.gate) cv *= gate_act(Raw16<T>::get(z[i], j), a.gate_act);
-          s[2] = fmaf(yv, yv, s[2]);
-          if (a.d_out) s[3] = fmaf(cv, Raw16<T>::get(dout[i], j), s[3]);
-          s[4] = fmaf(cv, u, s[4]);
-          s[5] = fmaf(cv, ov, s[5]);
-        }
+        s[2] = fmaf(yv, yv, s[2]);
+        s[3] = fmaf(cv, q.dout[i].get(j), s[3]);
+        s[4] = fmaf(cv, u, s[4]);
+        s[5] = fmaf(cv, ov, s[5]);
       }
+      q.o[i].renew();
+      q.dh[i].renew();
+      q.dout[i].renew();
+      q.y[i].renew();
     }
     sum(s);
-    const float r2 = rsqrtf(s[0] * inv_d + a.eps);
-    const float kap = a.next_gain ? r2 * r2 * r2 * (s[1] * inv_d) : 0.f;
-    const float r = a.post_gain ? rsqrtf(s[2] * inv_d + a.eps) : 1.f;
+    const float r2 = norm_next ? rsqrtf(s[0] * inv_d + a.eps) : 0.f;
+    const float kap = norm_next ? r2 * r2 * r2 * (s[1] * inv_d) : 0.f;
+    const float r = post ? rsqrtf(s[2] * inv_d + a.eps) : 1.f;
     const float m = r * r * ((s[3] + r2 * s[4] - kap * s[5]) * inv_d);   // r^2 sum(dn g y) / d
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = i * TEAM + lane;
-      if (c >= n8) continue;
-      float g1[8], g2[8], dx[8], dy[8], dz[8];
-      if (a.post_gain) load8(a.post_gain + c * 8, g1);
-      if (a.next_gain) load8(a.next_gain + c * 8, g2);
+      float dx[8], dy[8], dz[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        float D = a.d_out ? Raw16<T>::get(dout[i], j) : 0.f;
-        if (a.next_gain) {
-          const float ov = Raw16<T>::get(o[i], j), dhv = Raw16<T>::get(dh[i], j);
-          D += r2 * (dhv * g2[j]) - kap * ov;
-          acc_next[i][j] = fmaf(dhv, ov * r2, acc_next[i][j]);
-        }
+        const float ov = q.o[i].get(j), dhv = q.dh[i].get(j), yr = q.y[i].get(j) * r;
+        const float D = q.dout[i].get(j) + r2 * (dhv * g2[i][j]) - kap * ov;
+        const float up = a.branch_scale * D, dn = up * gate.a[i][j];
+        acc_next[i][j] = fmaf(dhv, ov * r2, acc_next[i][j]);
+        acc_post[i][j] = fmaf(dn, yr, acc_post[i][j]);
         dx[j] = a.res_scale * D;
-        if (a.y) {
-          const float yr = Raw16<T>::get(y[i], j) * r;
-          float dn = a.branch_scale * D;
-          if (a.gate) {
-            const float av = gate_act(Raw16<T>::get(z[i], j), a.gate_act);
-            dz[j] = dn * gate_slope(av, a.gate_act) * (a.post_gain ? yr * g1[j] : yr);
-            if (sums_gate) acc_gate[i][j] += dz[j];
-            dn *= av;
-          }
-          if (a.post_gain) {
-            acc_post[i][j] = fmaf(dn, yr, acc_post[i][j]);
-            dy[j] = r * (dn * g1[j]) - m * yr;
-          } else {
-            dy[j] = dn;
-          }
-        }
+        dz[j] = up * gate.slope[i][j] * (yr * g1[i][j]);
+        if (!TOKEN) acc_gate[i][j] += dz[j];
+        dy[j] = post ? r * (dn * g1[i][j]) - m * yr : dn;
       }
-      store8(static_cast<T*>(a.dx) + base + c * 8, dx);
-      if (a.y) store8(static_cast<T*>(a.dy) + base + c * 8, dy);
-      if (a.gate && !sums_gate) store8(static_cast<T*>(a.dgate) + base + c * 8, dz);
+      if (p.in[i]) {
+        store_row8<NT>(static_cast<T*>(a.dx) + base + p.col[i], dx);
+        if (a.y) store_row8<NT>(static_cast<T*>(a.dy) + base + p.col[i], dy);
+        if (TOKEN) store_row8<NT>(static_cast<T*>(a.dgate) + base + p.col[i], dz);
+      }
     }
     if (sums_gate && a.plan.teams_per_group == 0 && (t + 1 == hi || (t + 1) % period == 0)) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int c = i * TEAM + lane;
-        if (c < n8) store8(static_cast<float*>(a.dgate) + group * a.d + c * 8, acc_gate[i]);
+        if (p.in[i]) store8(static_cast<float*>(a.dgate) + gate.group * a.d + p.col[i], acc_gate[i]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) acc_gate[i][j] = 0.f;
       }
     }
+    if constexpr (kAhead) q = next;
+    else if (t + 1 < hi) load(q, t + 1);
   }
   const int64_t at = (int64_t)team * a.d;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int c = i * TEAM + lane;
-    if (c >= n8) continue;
-    if (a.post_gain) store8(a.part_post + at + c * 8, acc_post[i]);
-    if (a.next_gain) store8(a.part_next + at + c * 8, acc_next[i]);
-    if (a.plan.teams_per_group) store8(a.part_gate + at + c * 8, acc_gate[i]);
+    if (!p.in[i]) continue;
+    if (a.post_gain) store8(a.part_post + at + p.col[i], acc_post[i]);
+    if (a.next_gain) store8(a.part_next + at + p.col[i], acc_next[i]);
+    if (a.plan.teams_per_group) store8(a.part_gate + at + p.col[i], acc_gate[i]);
   }
 }
 
-// Column sums of the teams' parts, 64 columns a workgroup, four runs of teams added in
-// order.  blockIdx.y: the post gain, the next gain (those that there are), then the gate
-// groups whose rows several teams share.
-__global__ __launch_bounds__(256) void reduce_parts_kernel(BlockNormBackwardArgs a) {
-  __shared__ float buf[4][64];
+// Column sums of the teams' parts, 64 columns a workgroup: 64 runs of teams, one for every
+// 16 lanes of four columns each, then the runs in order.  blockIdx.y: the post gain, the next
+// gain (those that there are), then the gate groups whose rows several teams share.  (16
+// runs, a column a lane: 5.4 us for the two sums of 512 parts 1,024 wide, against 4.7.)
+constexpr int kRuns = 64;
+__global__ __launch_bounds__(16 * kRuns) void reduce_parts_kernel(BlockNormBackwardArgs a) {
+  __shared__ f32x4 buf[kRuns][16];
   int job = blockIdx.y;
   const float* part;
   float* dst;
@@ -345,47 +398,97 @@ __global__ __launch_bounds__(256) void reduce_parts_kernel(BlockNormBackwardArgs
     count = a.plan.teams_per_group;
     first = (int64_t)job * count;
   }
-  const int c = (int)blockIdx.x * 64 + (threadIdx.x & 63), run = threadIdx.x >> 6;
-  const int64_t per = (count + 3) / 4;
+  const int lane = threadIdx.x & 15, run = threadIdx.x >> 4, c = (int)blockIdx.x * 64 + lane * 4;
+  const int64_t per = (count + kRuns - 1) / kRuns;
   const int64_t lo = first + run * per, hi = lo + per < first + count ? lo + per : first + count;
-  float v = 0.f;
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 8
-  for (int64_t w = lo; w < hi; ++w) v += part[w * a.d + c];
-  buf[run][threadIdx.x & 63] = v;
+  for (int64_t w = lo; w < hi; ++w) v += *reinterpret_cast<const f32x4*>(part + w * a.d + c);
+  buf[run][lane] = v;
   __syncthreads();
-  if (run == 0) dst[c] = (buf[0][threadIdx.x] + buf[1][threadIdx.x]) + (buf[2][threadIdx.x] + buf[3][threadIdx.x]);
+  __shared__ f32x4 eight[8][16];
+  if (run < 8) {
+    v = buf[run * 8][lane];
+#pragma unroll
+    for (int q = 1; q < 8; ++q) v += buf[run * 8 + q][lane];
+    eight[run][lane] = v;
+  }
+  __syncthreads();
+  if (run == 0) {
+#pragma unroll
+    for (int q = 1; q < 8; ++q) v += eight[q][lane];
+    *reinterpret_cast<f32x4*>(dst + c) = v;
+  }
 }
 
-// The team that holds a row of d elements: the fewest threads that hold it in at most
-// four pieces of eight elements each, a whole workgroup above 1,024.
+// The team that holds a row of d elements: eight a lane up to 8,192, then sixteen.
 template <typename F> void by_width(int64_t d, F f) {
-  if (d <= 512) f(std::integral_constant<int, 64>{}, std::integral_constant<int, 1>{});
-  else if (d <= 1024) f(std::integral_constant<int, 64>{}, std::integral_constant<int, 2>{});
-  else if (d <= 2048) f(std::integral_constant<int, 256>{}, std::integral_constant<int, 1>{});
-  else if (d <= 4096) f(std::integral_constant<int, 256>{}, std::integral_constant<int, 2>{});
-  else if (d <= 6144) f(std::integral_constant<int, 256>{}, std::integral_constant<int, 3>{});
-  else if (d <= 8192) f(std::integral_constant<int, 256>{}, std::integral_constant<int, 4>{});
-  else f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 2>{});
+  using std::integral_constant;
+  if (d <= 512) f(integral_constant<int, 64>{}, integral_constant<int, 1>{});
+  else if (d <= 1024) f(integral_constant<int, 128>{}, integral_constant<int, 1>{});
+  else if (d <= 2048) f(integral_constant<int, 256>{}, integral_constant<int, 1>{});
+  else if (d <= 4096) f(integral_constant<int, 512>{}, integral_constant<int, 1>{});
+  else if (d <= 6144) f(integral_constant<int, 768>{}, integral_constant<int, 1>{});
+  else if (d <= 8192) f(integral_constant<int, 1024>{}, integral_constant<int, 1>{});
+  else f(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
+}
+
+// Rows go past the caches where one tensor of them is larger than what the caches hold of it
+// anyway (4 MB of L2 an XCD): 32 MB.
+bool past_caches(int64_t T, int64_t d, int dtype) { return T * d * (dtype == 1 ? 2 : 4) >= (int64_t(32) << 20); }
+
+template <typename T, int TEAM, int NV, bool NT, bool TOKEN>
+void launch_forward(const BlockNormArgs& a, int num_cu, hipStream_t stream) {
+  constexpr int threads = block_threads(TEAM), per = threads / TEAM;
+  // as many workgroups as a CU's 32 wavefronts hold (16: 352 us for 32,768 rows of 6,144, against 289)
+  const int64_t want = (a.T + per - 1) / per, most = (int64_t)num_cu * (32 / (threads / 64));
+  const dim3 grid((unsigned)(want < most ? want : most)), block(threads);
+  if (a.has_y && a.y == nullptr)
+    hipLaunchKernelGGL((block_norm_kernel<T, TEAM, NV, NT, true, TOKEN>), grid, block, 0, stream, a);
+  else
+    hipLaunchKernelGGL((block_norm_kernel<T, TEAM, NV, NT, false, TOKEN>), grid, block, 0, stream, a);
+}
+
+template <typename T, int TEAM, int NV, bool NT, bool TOKEN>
+void launch_backward(const BlockNormBackwardArgs& a, hipStream_t stream) {
+  constexpr int threads = block_threads(TEAM), per = threads / TEAM;
+  const dim3 grid((unsigned)((a.plan.teams + per - 1) / per)), block(threads);
+  hipLaunchKernelGGL((block_norm_backward_kernel<T, TEAM, NV, NT, TOKEN>), grid, block, 0, stream, a);
+}
+
+// f(nt, token) with both as types
+template <typename F> void by_flags(bool nt, bool token, F f) {
+  if (nt && token) f(std::true_type{}, std::true_type{});
+  else if (nt) f(std::true_type{}, std::false_type{});
+  else if (token) f(std::false_type{}, std::true_type{});
+  else f(std::false_type{}, std::false_type{});
 }
 
 }  // namespace
 
 hipError_t launch_block_norm(int dtype, const BlockNormArgs& a, int num_cu, hipStream_t stream) {
-  by_width(a.d, [&](auto team, auto nv) {
-    constexpr int TEAM = decltype(team)::value, NV = decltype(nv)::value;
-    const int per = TEAM < 256 ? 256 / TEAM : 1;
-    const int64_t want = (a.T + per - 1) / per, most = (int64_t)num_cu * 16;
-    const dim3 grid((unsigned)(want < most ? want : most)), block(TEAM < 256 ? 256 : TEAM);
-    if (dtype == 1) hipLaunchKernelGGL((block_norm_kernel<bf16, TEAM, NV>), grid, block, 0, stream, a);
-    else hipLaunchKernelGGL((block_norm_kernel<float, TEAM, NV>), grid, block, 0, stream, a);
+  by_flags(past_caches(a.T, a.d, dtype), a.gate && a.gate_rows == 1, [&](auto nt, auto token) {
+    by_width(a.d, [&](auto team, auto nv) {
+      constexpr int TEAM = decltype(team)::value, NV = decltype(nv)::value;
+      constexpr bool NT = decltype(nt)::value, TOKEN = decltype(token)::value;
+      if (dtype == 1) launch_forward<bf16, TEAM, NV, NT, TOKEN>(a, num_cu, stream);
+      else launch_forward<float, TEAM, NV, NT, TOKEN>(a, num_cu, stream);
+    });
   });
   return hipGetLastError();
 }
 
+// Teams of 12 wavefronts a CU on a card of 256 CUs (what their registers allow at once), but
+// two rows a team at least: each team writes one part of d floats a sum, which the second
+// kernel reads again (1,021 rows of 1,024 float32: one row a team 18.0 us, two 17.9, four 19.4).
 RowPlan block_norm_row_plan(int64_t T, int64_t d, int64_t gate_rows) {
-  // at most 512 workgroups' worth of teams: each team writes one part of d floats a sum
-  const int64_t teams = d <= 1024 ? 2048 : 512;
+  int64_t teams = 0;
+  by_width(d, [&](auto team, auto) {
+    constexpr int TEAM = decltype(team)::value, waves = TEAM / 64;
+    teams = 256 * (12 / waves > 0 ? 12 / waves : 1);
+  });
   int64_t rows = (T + teams - 1) / teams;
+  if (rows < 2) rows = 2;
   RowPlan p{};
   if (gate_rows <= 1 || gate_rows <= rows) {
     if (gate_rows > 1) rows = (rows + gate_rows - 1) / gate_rows * gate_rows;
@@ -402,19 +505,20 @@ RowPlan block_norm_row_plan(int64_t T, int64_t d, int64_t gate_rows) {
 }
 
 hipError_t launch_block_norm_backward(int dtype, const BlockNormBackwardArgs& a, hipStream_t stream) {
-  by_width(a.d, [&](auto team, auto nv) {
-    constexpr int TEAM = decltype(team)::value, NV = decltype(nv)::value;
-    const int per = TEAM < 256 ? 256 / TEAM : 1;
-    const dim3 grid((unsigned)((a.plan.teams + per - 1) / per)), block(TEAM < 256 ? 256 : TEAM);
-    if (dtype == 1) hipLaunchKernelGGL((block_norm_backward_kernel<bf16, TEAM, NV>), grid, block, 0, stream, a);
-    else hipLaunchKernelGGL((block_norm_backward_kernel<float, TEAM, NV>), grid, block, 0, stream, a);
+  by_flags(past_caches(a.T, a.d, dtype), a.gate && a.gate_rows == 1, [&](auto nt, auto token) {
+    by_width(a.d, [&](auto team, auto nv) {
+      constexpr int TEAM = decltype(team)::value, NV = decltype(nv)::value;
+      constexpr bool NT = decltype(nt)::value, TOKEN = decltype(token)::value;
+      if (dtype == 1) launch_backward<bf16, TEAM, NV, NT, TOKEN>(a, stream);
+      else launch_backward<float, TEAM, NV, NT, TOKEN>(a, stream);
+    });
   });
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
   const int64_t groups = a.plan.teams_per_group ? a.plan.teams / a.plan.teams_per_group : 0;
   const int64_t jobs = (a.post_gain != nullptr) + (a.next_gain != nullptr) + groups;
   if (jobs == 0) return hipSuccess;
-  hipLaunchKernelGGL(reduce_parts_kernel, dim3((unsigned)(a.d / 64), (unsigned)jobs), dim3(256), 0, stream, a);
+  hipLaunchKernelGGL(reduce_parts_kernel, dim3((unsigned)(a.d / 64), (unsigned)jobs), dim3(16 * kRuns), 0, stream, a);
   return hipGetLastError();
 }
 

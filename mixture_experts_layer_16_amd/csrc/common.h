@@ -29,6 +29,9 @@ template <typename T> struct Vec16 {
   static constexpr int N = 16 / sizeof(T);
 };
 
+// A workgroup barrier for LDS: loads into registers stay in flight (__syncthreads waits for them).
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
 __device__ __forceinline__ void wait_vmcnt0() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 }  // namespace moe

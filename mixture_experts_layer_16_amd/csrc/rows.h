@@ -49,6 +49,54 @@ __device__ __forceinline__ void store8(float* p, const float* v) {
   *reinterpret_cast<f32x4*>(p + 4) = b;
 }
 
+// Eight elements as loaded, in whole registers (a vector of 16-bit values that lives across a
+// loop's turns is taken apart into one register a value).
+template <typename T> struct Row8;
+template <> struct Row8<bf16> {
+  u32x4 v;
+  __device__ __forceinline__ float get(int i) const {
+    return __uint_as_float(i & 1 ? v[i >> 1] & 0xffff0000u : v[i >> 1] << 16);
+  }
+  // as if newly loaded: values converted before are not kept
+  __device__ __forceinline__ void renew() { asm volatile("" : "+v"(v)); }
+};
+template <> struct Row8<float> {
+  f32x4 a, b;
+  __device__ __forceinline__ float get(int i) const { return i < 4 ? a[i] : b[i - 4]; }
+  __device__ __forceinline__ void renew() {}
+};
+
+// Loads and stores of them; NT: past the caches, for rows that are read or written once and
+// are too many to be found in a cache again.
+template <bool NT> __device__ __forceinline__ void load_row8(Row8<bf16>& q, const bf16* p) {
+  const u32x4* s = reinterpret_cast<const u32x4*>(p);
+  if constexpr (NT) q.v = __builtin_nontemporal_load(s);
+  else q.v = *s;
+}
+template <bool NT> __device__ __forceinline__ void load_row8(Row8<float>& q, const float* p) {
+  const f32x4* s = reinterpret_cast<const f32x4*>(p);
+  if constexpr (NT) q = {__builtin_nontemporal_load(s), __builtin_nontemporal_load(s + 1)};
+  else q = {s[0], s[1]};
+}
+template <bool NT> __device__ __forceinline__ void store_row8(bf16* p, const float* v) {
+  if constexpr (NT) {
+    bf16x8 q;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = static_cast<bf16>(v[i]);
+    __builtin_nontemporal_store(q, reinterpret_cast<bf16x8*>(p));
+  } else {
+    store8(p, v);
+  }
+}
+template <bool NT> __device__ __forceinline__ void store_row8(float* p, const float* v) {
+  if constexpr (NT) {
+    __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, reinterpret_cast<f32x4*>(p));
+    __builtin_nontemporal_store(f32x4{v[4], v[5], v[6], v[7]}, reinterpret_cast<f32x4*>(p + 4));
+  } else {
+    store8(p, v);
+  }
+}
+
 // Sum over the 64 lanes of a wavefront; every lane ends with the same bits.
 __device__ __forceinline__ float wave_sum64(float v) {
 #pragma unroll

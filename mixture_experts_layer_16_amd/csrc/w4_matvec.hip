@@ -150,11 +150,6 @@ __device__ __forceinline__ void lds_order() {
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   __builtin_amdgcn_wave_barrier();
 }
-// A workgroup barrier for LDS: loads into registers stay in flight.
-__device__ __forceinline__ void lds_barrier() {
-  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-}
-
 // How the planes of a tile's rows are laid over MFMA rows.  Where SLOT rows of each plane
 // fit 16 together they share one MFMA (plane p of row r is MFMA row p * SLOT + r, and the
 // planes' results are added at the end); with SLOT 16 each plane has MFMAs of its own, which

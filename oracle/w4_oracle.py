@@ -4,7 +4,7 @@ TEST INFRASTRUCTURE ONLY.  Nothing in the product path may import, call or execu
 this module; it shares no code with the HIP path.
 
     W[r, c] = s[r, c // group] (q[r, c] - 8),  q in 0..15
-    s = bf16(max over the group |w| / 7),  q = 8 + round(w / s) clamped to 0..15
+    s = bf16(max over the group |w| * (1/7 in float32)),  q = 8 + round(w / s) clamped to 0..15
 
 Every product runs in float64 with numpy; the scale's rounding to bf16 is done on its
 bits.  products() also returns sum |s x| and sum |s (q - 8) x| of each result, which
@@ -33,7 +33,7 @@ def quantize(w, group):
     """(codes [.., C], scales [.., ceil(C/group)]) of w, both float64."""
     w = np.asarray(w, np.float64)
     g = groups_of(w, group)
-    s = round_bf16(np.abs(g).max(-1).astype(np.float32) / np.float32(7)).astype(np.float64)
+    s = round_bf16(np.abs(g).max(-1).astype(np.float32) * (np.float32(1) / np.float32(7))).astype(np.float64)
     q = np.rint(g / np.where(s > 0, s, 1.0)[..., None])
     q = np.where(s[..., None] > 0, np.clip(q, -8, 7), 0) + 8
     return q.reshape(w.shape[:-1] + (-1,))[..., :w.shape[-1]], s

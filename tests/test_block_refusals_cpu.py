@@ -72,16 +72,17 @@ def test_block_norm_backward_refuses(want, kw):
 
 
 def test_block_norm_backward_workspace():
-    # one part of d floats for a team and sum; rows are dealt to at most 2,048 teams (d <= 1,024) or 512
-    assert back(query=True) == (OK, 2 * 8 * 128 * 4)
-    assert back(query=True, next_gain=None) == (OK, 8 * 128 * 4)
+    # one part of d floats for a team and sum; two rows a team at least, and 12 wavefronts' teams for
+    # 256 CUs at most: 3,072 (d <= 512), 1,536 (<= 1,024), 768 (<= 2,048)
+    assert back(query=True) == (OK, 2 * 4 * 128 * 4)
+    assert back(query=True, next_gain=None) == (OK, 4 * 128 * 4)
     assert back(query=True, post_gain=None, next_gain=None) == (OK, 0)
-    assert back(query=True, T=4096, d=1024) == (OK, 2 * 2048 * 1024 * 4)
-    assert back(query=True, T=4096, d=1088) == (OK, 2 * 512 * 1088 * 4)
-    # 2,048 rows a gate group, 8 rows a team: 256 teams a group and their own parts
-    assert back(query=True, T=4096, d=1088, gate=P, gate_rows=2048) == (OK, 3 * 512 * 1088 * 4)
-    # groups of 3 rows: 9 rows a team, no parts of the gate
-    assert back(query=True, T=4096, d=1088, gate=P, gate_rows=3) == (OK, 2 * 456 * 1088 * 4)
+    assert back(query=True, T=4096, d=1024) == (OK, 2 * 1366 * 1024 * 4)
+    assert back(query=True, T=4096, d=1088) == (OK, 2 * 683 * 1088 * 4)
+    # 2,048 rows a gate group, 6 rows a team: 342 teams a group and their own parts
+    assert back(query=True, T=4096, d=1088, gate=P, gate_rows=2048) == (OK, 3 * 684 * 1088 * 4)
+    # groups of 4 rows: 8 rows a team, no parts of the gate
+    assert back(query=True, T=4096, d=1088, gate=P, gate_rows=4) == (OK, 2 * 512 * 1088 * 4)
 
 
 def w4(fn, **kw):

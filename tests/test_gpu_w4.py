@@ -74,6 +74,10 @@ def test_quantize_gives_the_oracles_values(n, R, C, group, dt):
     want = torch.from_numpy(w4o.values(q, s, group))
     assert bits_equal(got.dequantize(FP).cpu() + 0.0, want.to(FP) + 0.0)     # 12 bits: exact in float32
     assert torch.equal(got.dequantize(BF).cpu(), want.to(BF))
+    # and the same buffers as the oracle's codes and scales packed, what pads them included
+    q, s = torch.from_numpy(q).to(DEV, torch.uint8), torch.from_numpy(s).to(DEV, BF)
+    same = B.moe_w4_pack(q[..., 0::2] | q[..., 1::2] << 4, s, group)
+    assert torch.equal(got.codes, same.codes) and bits_equal(got.scales, same.scales)
 
 
 def test_quantize_next_to_a_half_goes_by_the_exact_quotient():
@@ -83,7 +87,9 @@ def test_quantize_next_to_a_half_goes_by_the_exact_quotient():
     w = np.zeros((3, 32), np.float32)
     w[:, 0] = 7
     w[0, 1:15], w[1, 1:15], w[2, 1:15] = base, np.nextafter(base, np.float32(99)), np.nextafter(base, np.float32(-99))
-    w = np.concatenate([w, w * np.float32(2 ** -20), w * np.float32(1.7109375)])   # another scale, exact in bf16
+    # other scales, exact in bf16: small, subnormal ones (bf16 2^-130) and large
+    w = np.concatenate([w] + [w * np.float32(f) for f in (2.0 ** -20, 1.7109375, 2.0 ** -100, 2.0 ** 120)]
+                       + [(w.astype(np.float64) * 2.0 ** -126).astype(np.float32)])
     got = B.moe_w4_quantize(torch.from_numpy(w).to(DEV), 32).dequantize(FP)
     q, sc = w4o.quantize(w, 32)
     assert np.array_equal(f64(got)[0], w4o.values(q, sc, 32))
