@@ -121,9 +121,9 @@ struct BlockNormArgs {
 };
 hipError_t launch_block_norm(int dtype, const BlockNormArgs& a, int num_cu, hipStream_t stream);
 
-// How the backward deals rows to teams: `rows` consecutive rows each; with
-// teams_per_group > 0 each gate group has that many teams of its own, otherwise a
-// team's rows cover whole groups.
+// How the backward deals rows to teams, `rows` each at most: with teams_per_group > 0 each
+// gate group has that many teams of its own; otherwise a team's rows are consecutive and
+// cover whole groups, or any without a group to share.
 struct RowPlan {
   int teams;
   int teams_per_group;

@@ -104,4 +104,20 @@ __device__ __forceinline__ float wave_sum64(float v) {
   return v;
 }
 
+// The same sum in registers only: shifts inside each row of 16 lanes, then the rows' totals
+// passed on to the last lane, and from there to all (in a scalar register).  Six steps of a few
+// cycles, where a step through the LDS crossbar takes some sixty.
+__device__ __forceinline__ float wave_total(float v) {
+#define MOE_SUM_STEP(ctrl, rows) \
+  v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), ctrl, rows, 0xf, false))
+  MOE_SUM_STEP(0x111, 0xf);   // row_shr:1
+  MOE_SUM_STEP(0x112, 0xf);   // row_shr:2
+  MOE_SUM_STEP(0x114, 0xf);   // row_shr:4
+  MOE_SUM_STEP(0x118, 0xf);   // row_shr:8
+  MOE_SUM_STEP(0x142, 0xa);   // row_bcast:15
+  MOE_SUM_STEP(0x143, 0xc);   // row_bcast:31
+#undef MOE_SUM_STEP
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+
 }  // namespace moe

@@ -73,9 +73,11 @@ template <typename F> __device__ __forceinline__ int lane_scan(int v, int identi
 __device__ __forceinline__ TokenTile find_tile(const int32_t* offsets, int E, int64_t n_max, int slot) {
   const int lane = threadIdx.x & 63;
   int prev = offsets[0], base = 0;
+  int ahead = lane < E ? offsets[lane + 1] : 0;
   for (int e0 = 0; e0 < E; e0 += 64) {
     const int e = e0 + lane;
-    const int raw = e < E ? offsets[e + 1] : prev;
+    const int raw = e < E ? ahead : prev;
+    if (e + 64 < E) ahead = offsets[e + 65];
     const int top = lane_scan(raw > prev ? raw : prev, INT32_MIN, [](int a, int b) { return a > b ? a : b; });
     int below = __shfl_up(top, 1, 64);
     if (lane == 0) below = prev;
@@ -176,7 +178,16 @@ template <int PLANES, int SLOT> struct RowLoads {
   uint32_t off[RG], last[RG];                  // in the last column tile, columns past the row are not there either
   uint32_t plane;                              // bytes between planes
   int put[RG], KT;
+  // the rows' numbers; whoever comes next can be on its way before they arrive
   __device__ __forceinline__ RowLoads(const W4Args& a, int row0, int rows) : KT(a.KT) {
+    const int quad = (threadIdx.x & 63) >> 4;
+#pragma unroll
+    for (int g = 0; g < RG; ++g) {
+      const int r = L::kPacked ? (g * 4 + quad) % SLOT : g * 4 + quad;
+      off[g] = r < rows ? (a.a_rows ? a.a_rows[row0 + r] : row0 + r) : 0;
+    }
+  }
+  __device__ __forceinline__ void place(const W4Args& a, int rows) {
     const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4;
     const bool cut = (a.KT - 1) * kW4Cols + col * 8 >= a.C;
     plane = (uint32_t)a.n_in * (uint32_t)(a.C * 2);
@@ -184,10 +195,9 @@ template <int PLANES, int SLOT> struct RowLoads {
 #pragma unroll
     for (int g = 0; g < RG; ++g) {
       const int v = g * 4 + quad, r = L::kPacked ? v % SLOT : v;
-      off[g] = kNowhere;                       // rows that are not there load nothing, and so zeros
-      if (r < rows)
-        off[g] = (uint32_t)(a.a_rows ? clamp_row(a.a_rows[row0 + r], a.n_in) : row0 + r) * (uint32_t)(a.C * 2) +
-                 col * 16 + (L::kPacked ? v / SLOT * plane : 0u);
+      const uint32_t at = (uint32_t)clamp_row((int)off[g], a.n_in) * (uint32_t)(a.C * 2) + col * 16 +
+                          (L::kPacked ? v / SLOT * plane : 0u);
+      off[g] = r < rows ? at : kNowhere;       // rows that are not there load nothing, and so zeros
       last[g] = cut ? kNowhere : off[g];
       put[g] = v * 256 + ((col ^ v) * 16);
     }
@@ -290,7 +300,7 @@ __device__ __forceinline__ void stream(const W4Args& a, const Streams<NT, GPT, S
   using L = Rows<PLANES, SLOT>;
   constexpr bool FINE = PLANES == 3;
   constexpr int SB = 4 / GPT < DEPTH ? 4 / GPT : DEPTH;       // column tiles of a scale load
-  const RowLoads<PLANES, SLOT> rl(a, row0, rows);
+  RowLoads<PLANES, SLOT> rl(a, row0, rows);
   const bf16x8 minus = offset_operand<FINE>();
   const UnpackConstants consts;
   u32x4 w[DEPTH][NT];
@@ -305,12 +315,13 @@ __device__ __forceinline__ void stream(const W4Args& a, const Streams<NT, GPT, S
       if (tile < CH) rl.store(x, lds + (half * CH + tile) * L::kTile + unit * 4096);
       lds_barrier();
     };
-    rl.load(x, unit, tile);
 #pragma unroll
     for (int u = 0; u < DEPTH; ++u) {
       from.load(w[u], u);
       if (u % SB == 0) from.template load_scales_of<SB>(s[u / SB], u);
     }
+    rl.place(a, rows);
+    rl.load(x, unit, tile);
     put(0);
     int half = 0;
     for (int k = 0; k < from.n; k += U) {
@@ -335,9 +346,11 @@ __device__ __forceinline__ void stream(const W4Args& a, const Streams<NT, GPT, S
 #pragma unroll
     for (int u = 0; u < DEPTH; ++u) {
       from.load(w[u], u);
-      load_x(u, k0 + u);
       if (u % SB == 0) from.template load_scales_of<SB>(s[u / SB], u);
     }
+    rl.place(a, rows);
+#pragma unroll
+    for (int u = 0; u < DEPTH; ++u) load_x(u, k0 + u);
     for (int k = 0; k < from.n; k += DEPTH) {
 #pragma unroll
       for (int u = 0; u < DEPTH; ++u) {
