@@ -15,7 +15,8 @@
 // The offsets (136 or 24 with the code's own 8) are taken out by the matrix unit too:
 // a group's accumulators start at x . (-136 | -24), one MFMA with a constant B operand
 // shared by every tile of the wavefront, instead of at zero.  What is then left per
-// group is total += s * acc, one FMA a result.  All sums are float32.
+// group is total += s * acc, one FMA a result.  All sums are float32.  Float32 results
+// take codes without an offset instead (unpack_exact).
 //
 // A operands are bf16 planes whose sum is the float32 activation: one plane for bf16
 // activations, three for float32 ones (24 bits), two for the hidden activations of a
@@ -98,28 +99,39 @@ __device__ __forceinline__ TokenTile find_tile(const int32_t* offsets, int E, in
   return {-1, 0, 0};
 }
 
-// Eight codes -> eight bf16: 128 + q in elements 0 and 1, 16 + q in the others; FINE:
-// 16 + q throughout (one shift more; the smaller offset keeps four times less rounding
-// of the group sums, which float32 results show and bf16 ones do not).  The constants are
-// registers (as literals, of which an instruction holds one, each and-or became two
-// instructions): the masks vector ones, the exponents scalar ones.
+// Eight codes -> eight bf16: 128 + q in elements 0 and 1, 16 + q in the others.  The
+// constants are registers (as literals, of which an instruction holds one, each and-or
+// became two instructions): the masks vector ones, the exponents scalar ones.
 struct UnpackConstants {
   uint32_t mask0, mask3, exp7, exp4;
   __device__ __forceinline__ UnpackConstants() : mask0(0x000f000fu), mask3(0x00780078u), exp7(0x43004300u), exp4(0x41804180u) {
     asm("" : "+v"(mask0), "+v"(mask3), "+s"(exp7), "+s"(exp4));
   }
 };
-template <bool FINE> __device__ __forceinline__ bf16x8 unpack(uint32_t u, const UnpackConstants& k) {
-  u32x4 v;
-  v[0] = FINE ? ((u << 3) & k.mask3) | k.exp4 : (u & k.mask0) | k.exp7;
-  v[1] = ((u >> 1) & k.mask3) | k.exp4;
-  v[2] = ((u >> 5) & k.mask3) | k.exp4;
-  v[3] = ((u >> 9) & k.mask3) | k.exp4;
+__device__ __forceinline__ bf16x8 unpack(uint32_t u, const UnpackConstants& k) {
+  const u32x4 v = {(u & k.mask0) | k.exp7, ((u >> 1) & k.mask3) | k.exp4, ((u >> 5) & k.mask3) | k.exp4,
+                   ((u >> 9) & k.mask3) | k.exp4};
   return __builtin_bit_cast(bf16x8, v);
 }
-template <bool FINE> __device__ __forceinline__ bf16x8 offset_operand() {
+__device__ __forceinline__ bf16x8 offset_operand() {
   constexpr uint32_t m136 = 0xc308c308u, m24 = 0xc1c0c1c0u;   // -136, -24 in both halves
-  const u32x4 v = {FINE ? m24 : m136, m24, m24, m24};
+  const u32x4 v = {m136, m24, m24, m24};
+  return __builtin_bit_cast(bf16x8, v);
+}
+
+// The same without an offset, (q - 8) / 16 in every element, for float32 results: sums
+// that carry an offset round to the offset's size, which bf16 results do not show.  (With
+// 16 + q throughout, float32 products of 4,800 columns were off by 1.5e-6 of their norm;
+// so by 1.4e-7, a plain float32 product by 5.6e-7, and as fast: 33 x 4096 x 4096 in 22.2 us
+// against 21.7.)  v_cvt_off_f32_i4 takes a signed code, so q with its top bit the other
+// way, to that sixteenth, whose high half is a bf16; the 16 is put back a group at a time.
+__device__ __forceinline__ bf16x8 unpack_exact(uint32_t u) {
+  u ^= 0x88888888u;
+  u32x4 v;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    v[j] = __builtin_amdgcn_perm(__float_as_uint(__builtin_amdgcn_cvt_off_f32_i4((int)(u >> (4 * j + 16)))),
+                                 __float_as_uint(__builtin_amdgcn_cvt_off_f32_i4((int)(u >> (4 * j)))), 0x07060302u);
   return __builtin_bit_cast(bf16x8, v);
 }
 
@@ -216,7 +228,7 @@ template <int PLANES, int SLOT> struct RowLoads {
 
 // One column tile of NT streams of weights against an LDS tile of rows.  s holds the scales
 // of the streams' groups, this tile's from group s_at on.
-template <int MP, bool FINE, int GPT, int NT>
+template <int MP, bool EXACT, int GPT, int NT>
 __device__ __forceinline__ void multiply_tile(const char* tile, const u32x4 (&w)[NT], const uint2 (&s)[NT], int s_at,
                                               bf16x8 minus, const UnpackConstants& consts, f32x4 (&total)[NT]) {
   constexpr int M = 4 / GPT;         // MFMAs of a group
@@ -230,22 +242,24 @@ __device__ __forceinline__ void multiply_tile(const char* tile, const u32x4 (&w)
 #pragma unroll
   for (int g = 0; g < GPT; ++g) {
     f32x4 c0 = {0.f, 0.f, 0.f, 0.f};
+    if constexpr (!EXACT) {
 #pragma unroll
-    for (int i = g * M; i < (g + 1) * M; ++i)
+      for (int i = g * M; i < (g + 1) * M; ++i)
 #pragma unroll
-      for (int p = 0; p < MP; ++p) c0 = mfma(b[p][i], minus, c0);
+        for (int p = 0; p < MP; ++p) c0 = mfma(b[p][i], minus, c0);
+    }
 #pragma unroll
     for (int m = 0; m < NT; ++m) {
       f32x4 acc = c0;
 #pragma unroll
       for (int i = g * M; i < (g + 1) * M; ++i) {
-        const bf16x8 wf = unpack<FINE>(w[m][i], consts);
+        const bf16x8 wf = EXACT ? unpack_exact(w[m][i]) : unpack(w[m][i], consts);
 #pragma unroll
         for (int p = 0; p < MP; ++p) acc = mfma(b[p][i], wf, acc);
       }
       const float sc = scale_at(s[m], s_at + g);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) total[m][i] = fmaf(sc, acc[i], total[m][i]);
+      for (int i = 0; i < 4; ++i) total[m][i] = fmaf(sc, EXACT ? acc[i] * 16.f : acc[i], total[m][i]);
     }
   }
   // the sums are due here: moved behind the loop's other tiles they would keep every
@@ -298,10 +312,10 @@ template <int PLANES, int SLOT, int GPT, int NT, int DEPTH, bool SHARED, bool SW
 __device__ __forceinline__ void stream(const W4Args& a, const Streams<NT, GPT, SWIGLU>& from, int k0, int row0, int rows,
                                        char* lds, f32x4 (&total)[NT]) {
   using L = Rows<PLANES, SLOT>;
-  constexpr bool FINE = PLANES == 3;
+  constexpr bool EXACT = PLANES == 3;
   constexpr int SB = 4 / GPT < DEPTH ? 4 / GPT : DEPTH;       // column tiles of a scale load
   RowLoads<PLANES, SLOT> rl(a, row0, rows);
-  const bf16x8 minus = offset_operand<FINE>();
+  const bf16x8 minus = offset_operand();
   const UnpackConstants consts;
   u32x4 w[DEPTH][NT];
   uint2 s[DEPTH / SB][NT];
@@ -329,7 +343,7 @@ __device__ __forceinline__ void stream(const W4Args& a, const Streams<NT, GPT, S
       for (int v = 0; v < U; ++v) {
         const int u = v % DEPTH;
         if (v % CH == 0) rl.load(x, unit, k + v + CH + tile);
-        multiply_tile<L::kUnits, FINE, GPT, NT>(lds + (half * CH + v % CH) * L::kTile, w[u], s[u / SB], u % SB * GPT,
+        multiply_tile<L::kUnits, EXACT, GPT, NT>(lds + (half * CH + v % CH) * L::kTile, w[u], s[u / SB], u % SB * GPT,
                                                 minus, consts, total);
         from.load(w[u], k + v + DEPTH);
         if (u % SB == SB - 1) from.template load_scales_of<SB>(s[u / SB], k + v + 1 - SB + DEPTH);
@@ -358,7 +372,7 @@ __device__ __forceinline__ void stream(const W4Args& a, const Streams<NT, GPT, S
 #pragma unroll
         for (int q = 0; q < L::kUnits; ++q) rl.store(x[u][q], lds + q * 4096);
         lds_order();
-        multiply_tile<L::kUnits, FINE, GPT, NT>(lds, w[u], s[u / SB], u % SB * GPT, minus, consts, total);
+        multiply_tile<L::kUnits, EXACT, GPT, NT>(lds, w[u], s[u / SB], u % SB * GPT, minus, consts, total);
         from.load(w[u], k + u + DEPTH);
         load_x(u, k0 + k + u + DEPTH);
         if (u % SB == SB - 1) from.template load_scales_of<SB>(s[u / SB], k + u + 1 - SB + DEPTH);

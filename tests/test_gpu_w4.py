@@ -3,13 +3,13 @@
 Tolerance of a product's element y = sum_c s (q - 8) x (u = 2^-24, half = half a step of
 the output's type: bf16 2^-8, float32 2^-24):
 
-    |g - y| <= half |y| + 48 u A sum|s x| + (C/128 + 8) u sum|s (q - 8) x| + 2^-23 sum|s (q - 8) x|
+    |g - y| <= half |y| + 48 u P + (C/128 + 8) u sum|s (q - 8) x| + 2^-23 sum|s (q - 8) x|
 
-The codes enter the sums as 128 + q or 16 + q with the offset taken out inside a group:
-a group's partial sums are at most A sum|x|, A = 136 + 143 where a part of the codes is
-128 + q (bf16 activations), A = 24 + 31 where none is (float32); 32 products of an MFMA
-and at most 12 MFMAs that follow one another round each partial sum, 48 in all.  The
-groups' totals are then added C/128 times and over four wavefronts.  Float32 activations
+P is what a group's partial sums are at most.  With bf16 activations the codes enter the
+sums as 128 + q or 16 + q with the offset taken out inside a group: P = A sum|s x|,
+A = 136 + 143.  With float32 ones they enter as q - 8: P = sum|s (q - 8) x|.  32 products
+of an MFMA and at most 12 MFMAs that follow one another round each partial sum, 48 in all.
+The groups' totals are then added C/128 times and over four wavefronts.  Float32 activations
 are three bf16 numbers whose sum is within 2^-24 of them; 2^-23 holds that and the
 second plane's 2^-16 of the hidden activations is counted where they are.
 """
@@ -45,8 +45,7 @@ def packed(n, R, C, group, seed=0, scale=None):
 def product_bound(x, q, s, group, dt):
     """(y, error of the float32 evaluation)"""
     y, sx, swx = w4o.products(x, q, s, group)
-    A = 279.0 if dt == BF else 55.0
-    return y, 48 * U * A * sx + (q.shape[-1] / 128 + 8) * U * swx + 2.0 ** -23 * swx
+    return y, 48 * U * (279.0 * sx if dt == BF else swx) + (q.shape[-1] / 128 + 8) * U * swx + 2.0 ** -23 * swx
 
 
 def check(g, o, err, dt, what):
