@@ -8,7 +8,6 @@ no fallback of any kind, and a missing library is an error.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -378,9 +377,14 @@ def moe_layer_forward(x, w_router, bias, w_gate, w_up, w_down, k: int, topk_ids=
     return L
 
 
-def _on(dev: torch.device):
-    """Makes dev the current device for a launch if another one is."""
-    return torch.cuda.device(dev) if dev.index != torch.cuda.current_device() else contextlib.nullcontext()
+def _launch(name: str, fn, dev: torch.device, *args):
+    """One call on dev's current stream, with dev as the current device."""
+    if dev.index == torch.cuda.current_device():
+        st = fn(*args, _raw_stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, _raw_stream(dev))
+    _check(name, st)
 
 
 def _same(name: str, t: Optional[torch.Tensor], dev, dtype, shape):
@@ -445,8 +449,7 @@ class BlockNorm:
                      _p(self.h), _p(self.y_out))
 
     def __call__(self):
-        with _on(self.dev):
-            _check("moe_block_norm", lib().moe_block_norm(*self.args, _raw_stream(self.dev)))
+        _launch("moe_block_norm", lib().moe_block_norm, self.dev, *self.args)
         return self
 
 
@@ -495,9 +498,8 @@ class BlockNormBackward:
         self._ws_p = _p(self.ws)
 
     def __call__(self):
-        with _on(self.dev):
-            _check("moe_block_norm_backward",
-                   lib().moe_block_norm_backward(*self.args, self._ws_p, ctypes.byref(self._n), _raw_stream(self.dev)))
+        _launch("moe_block_norm_backward", lib().moe_block_norm_backward, self.dev, *self.args, self._ws_p,
+                ctypes.byref(self._n))
         return self
 
 
@@ -530,10 +532,8 @@ class W4Weights:
         if out is None:
             out = torch.empty(self.n, self.R, self.C, dtype=dtype, device=dev)
         _same("out", out, dev, out.dtype, (self.n, self.R, self.C))
-        with _on(dev):
-            _check("moe_w4_dequantize",
-                   lib().moe_w4_dequantize(self.n, self.R, self.C, dtype_code(out.dtype), self.group, _p(self.codes),
-                                           _p(self.scales), _p(out), _raw_stream(dev)))
+        _launch("moe_w4_dequantize", lib().moe_w4_dequantize, dev, self.n, self.R, self.C, dtype_code(out.dtype),
+                self.group, _p(self.codes), _p(self.scales), _p(out))
         return out
 
 
@@ -547,9 +547,7 @@ class W4Quantize:
         self.args = (n, R, C, dtype_code(w.dtype), group, _p(self.w), _p(self.out.codes), _p(self.out.scales))
 
     def __call__(self) -> W4Weights:
-        dev = self.w.device
-        with _on(dev):
-            _check("moe_w4_quantize", lib().moe_w4_quantize(*self.args, _raw_stream(dev)))
+        _launch("moe_w4_quantize", lib().moe_w4_quantize, self.w.device, *self.args)
         return self.out
 
 
@@ -566,9 +564,7 @@ def moe_w4_pack(q, s, group: int = 128) -> W4Weights:
     out = W4Weights(n, R, 2 * half, group, dev)
     _same("q", q, dev, torch.uint8, (n, R, half))
     _same("s", s, dev, torch.bfloat16, (n, R, -(-2 * half // group)))
-    with _on(dev):
-        _check("moe_w4_pack", lib().moe_w4_pack(n, R, 2 * half, group, _p(q), _p(s), _p(out.codes), _p(out.scales),
-                                                _raw_stream(dev)))
+    _launch("moe_w4_pack", lib().moe_w4_pack, dev, n, R, 2 * half, group, _p(q), _p(s), _p(out.codes), _p(out.scales))
     return out
 
 
@@ -592,9 +588,7 @@ class W4Matvec:
         self._ws_p = _p(self.ws)
 
     def __call__(self):
-        with _on(self.dev):
-            _check("moe_w4_matvec", lib().moe_w4_matvec(*self.args, self._ws_p, ctypes.byref(self._n),
-                                                        _raw_stream(self.dev)))
+        _launch("moe_w4_matvec", lib().moe_w4_matvec, self.dev, *self.args, self._ws_p, ctypes.byref(self._n))
         return self.y
 
 
@@ -639,9 +633,8 @@ class W4GroupedFfn:
         self._ws_p = _p(self.ws)
 
     def __call__(self):
-        with _on(self.dev):
-            _check("moe_w4_grouped_ffn", lib().moe_w4_grouped_ffn(*self.args, self._ws_p, ctypes.byref(self._n),
-                                                                  _raw_stream(self.dev)))
+        _launch("moe_w4_grouped_ffn", lib().moe_w4_grouped_ffn, self.dev, *self.args, self._ws_p,
+                ctypes.byref(self._n))
         return self.y_perm
 
 
