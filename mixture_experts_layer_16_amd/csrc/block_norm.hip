@@ -10,10 +10,12 @@
 // out = x: the norm before a first block.
 //
 // A row lives in the registers of one team: eight of its elements a lane (sixteen above
-// 8,192), so a team is as many wavefronts as the row needs.  Teams walk over rows with the
-// gains in registers and the next row's loads in flight; every tensor is read once and
-// written once, and all that crosses lanes are the row sums.  What bounds the kernels is
-// memory, and for a few rows the latency of one load, two row sums and one store.
+// 8,192), so a team is as many wavefronts as the row needs, or 8, 16 or 32 lanes of one.
+// Teams walk over rows with the gains in registers and the next row's loads in flight; every
+// tensor is read once and written once, and all that crosses lanes are the row sums.  What
+// bounds the kernels is memory, and for a few rows the latency of one load, two row sums and
+// one store.  Forward, 32,768 rows of 6,144 bf16: 290 us, 5.6 TB/s (the same bytes copied with
+// the same hints: 6.0); one row 3.2 us.
 #include "common.h"
 #include "kernels.h"
 #include "rows.h"
@@ -36,16 +38,28 @@ __device__ __forceinline__ float gate_slope(float a, int act) {
   return 1.f;
 }
 
+constexpr int block_threads(int team) { return team <= 64 ? 256 : team; }
+constexpr int waves_of(int team) { return team <= 64 ? 1 : team / 64; }
+
+// This thread's team: a scalar where all lanes of a wavefront are of one.
+template <int TEAM> __device__ __forceinline__ int own_team() {
+  constexpr int kTeams = block_threads(TEAM) / TEAM;
+  if constexpr (kTeams == 1) return (int)blockIdx.x;
+  const int team = (int)blockIdx.x * kTeams + (int)threadIdx.x / TEAM;
+  return TEAM < 64 ? team : __builtin_amdgcn_readfirstlane(team);
+}
+
 // Sums of NS values over a team of TEAM threads (a workgroup, where it is more than one
-// wavefront); every thread ends with the same bits.  Two buffers in turn: a wavefront
+// wavefront; otherwise a wavefront or 8, 16 or 32 lanes of one); every thread ends with the
+// same bits.  Two buffers in turn: a wavefront
 // writes a buffer again only after the barrier of the sum in between, which all others
 // reach after reading it.
 template <int TEAM, int NS> struct TeamSum {
-  float (*buf)[NS][TEAM / 64];
+  float (*buf)[NS][waves_of(TEAM)];
   int turn = 0;
   __device__ __forceinline__ void operator()(float* v) {
 #pragma unroll
-    for (int s = 0; s < NS; ++s) v[s] = wave_total(v[s]);
+    for (int s = 0; s < NS; ++s) v[s] = lanes_total<TEAM < 64 ? TEAM : 64>(v[s]);
     if constexpr (TEAM > 64) {
       const int wave = threadIdx.x >> 6;
       if ((threadIdx.x & 63) == 0) {
@@ -64,7 +78,6 @@ template <int TEAM, int NS> struct TeamSum {
   }
 };
 
-constexpr int block_threads(int team) { return team < 256 && team == 64 ? 256 : team; }
 
 // This lane's pieces of a row: piece i is elements (i * TEAM + lane) * 8 .. + 7.
 template <int TEAM, int NV> struct Pieces {
@@ -89,13 +102,10 @@ template <int TEAM, int NV> struct Pieces {
   }
 };
 
-// The gate's values for the row's group, computed again only where the group changes.
+// The gate's values for a group's row.
 template <typename T, int TEAM, int NV> struct Gate {
   float a[NV][8];
-  int64_t group = -1;
   __device__ __forceinline__ void at(const Pieces<TEAM, NV>& p, const void* gate, int64_t g, int d, int act) {
-    if (g == group) return;
-    group = g;
     Row8<T> z[NV] = {};
     p.template load<false>(z, static_cast<const T*>(gate) + g * d);
     from(z, act);
@@ -117,9 +127,9 @@ template <typename T, int TEAM, int NV> struct Gate {
 template <typename T, int TEAM, int NV, bool NT, bool COMBINE, bool TOKEN>
 __global__ __launch_bounds__(block_threads(TEAM)) void block_norm_kernel(BlockNormArgs a) {
   constexpr int kTeams = block_threads(TEAM) / TEAM;
-  __shared__ float buf[2][1][TEAM / 64];
+  __shared__ float buf[2][1][waves_of(TEAM)];
   TeamSum<TEAM, 1> sum{buf};
-  const int team = __builtin_amdgcn_readfirstlane((int)blockIdx.x * kTeams + (kTeams > 1 ? (int)threadIdx.x / TEAM : 0));
+  const int team = own_team<TEAM>();
   const int64_t step = (int64_t)gridDim.x * kTeams;
   const Pieces<TEAM, NV> p(a.d);
   const float inv_d = 1.f / (float)a.d;
@@ -136,6 +146,7 @@ __global__ __launch_bounds__(block_threads(TEAM)) void block_norm_kernel(BlockNo
   if (a.post_gain) p.gains(g1, a.post_gain);
   if (a.next_gain) p.gains(g2, a.next_gain);
   Gate<T, TEAM, NV> gate;
+  int64_t gate_end = 0;                        // of the group whose values these are
   for (int64_t t = team; t < a.T; t += step) {
     const int64_t base = t * a.d;
     if (t + step < a.T) {
@@ -161,7 +172,8 @@ __global__ __launch_bounds__(block_threads(TEAM)) void block_norm_kernel(BlockNo
           float w[4];
 #pragma unroll
           for (int s = 0; s < 4; ++s) {
-            const int row = s0 + s < a.k ? __builtin_amdgcn_readfirstlane(a.slot_row[t * a.k + s0 + s]) : -1;
+            int row = s0 + s < a.k ? a.slot_row[t * a.k + s0 + s] : -1;
+            if (TEAM >= 64) row = __builtin_amdgcn_readfirstlane(row);
             const bool there = (unsigned)row < (unsigned)a.n_rows;
             w[s] = there ? a.topk_w[t * a.k + s0 + s] : 0.f;
             if (there) p.template load<NT>(e[s], yp + (int64_t)row * a.d);
@@ -197,7 +209,11 @@ __global__ __launch_bounds__(block_threads(TEAM)) void block_norm_kernel(BlockNo
         r *= rsqrtf(ss * inv_d + a.eps);
       }
       if constexpr (TOKEN) gate.from(z, a.gate_act);
-      else if (a.gate) gate.at(p, a.gate, (int64_t)((uint64_t)t / (uint64_t)a.gate_rows), a.d, a.gate_act);
+      else if (a.gate && t >= gate_end) {
+        const uint64_t g = (uint64_t)t / (uint64_t)a.gate_rows, rows = (uint64_t)a.gate_rows;
+        gate.at(p, a.gate, (int64_t)g, a.d, a.gate_act);
+        gate_end = g + 1 > (uint64_t)a.T / rows ? a.T : (int64_t)((g + 1) * rows);
+      }
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         if (!p.in[i]) continue;
@@ -249,8 +265,8 @@ __global__ __launch_bounds__(block_threads(TEAM)) void block_norm_kernel(BlockNo
 // sum(c o): all six row sums (those three, o^2, y^2, dh g2 o) are taken at once, and neither
 // norm's statistics need to be kept by the forward.
 //
-// A team keeps the column sums of its rows in registers; they go out once at its end, and a
-// second kernel adds the teams' parts in order (no atomics).  Rows are dealt so that a team's
+// A team keeps the column sums of its rows in registers; they go out once at its end (one
+// part for the teams of a workgroup), and a second kernel adds the parts in order (no atomics).  Rows are dealt so that a team's
 // either cover whole gate groups or lie in one (RowPlan), and the teams' rows next to one
 // another where they can: with a run of its own for each team, 16,384 rows of 6,144 bf16
 // took 252 us instead of 231 (1.22 GB, 5.3 TB/s; the same bytes copied with the same hints: 6.1).
@@ -262,18 +278,42 @@ __global__ __launch_bounds__(block_threads(TEAM)) void block_norm_kernel(BlockNo
 //
 // What is absent is computed with as zeros (a gain or gate as ones): branches inside the
 // row cost more registers than the arithmetic costs time.
+//
+// A value of every team of a workgroup summed into its first team's, the others' zero.
+template <int TEAM> __device__ __forceinline__ void join(float (&v)[8], f32x4 (*buf)[TEAM < 64 ? TEAM : 64][2]) {
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+#pragma unroll
+  for (int o = TEAM; o < 64; o *= 2)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += __shfl_xor(v[j], o, 64);
+  if (lane < TEAM) {
+    buf[wave][lane][0] = f32x4{v[0], v[1], v[2], v[3]};
+    buf[wave][lane][1] = f32x4{v[4], v[5], v[6], v[7]};
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    v[j] = 0.f;
+    if (threadIdx.x < TEAM)
+#pragma unroll
+      for (int w = 0; w < 4; ++w) v[j] += buf[w][lane][j / 4][j % 4];
+  }
+  __syncthreads();
+}
+
 template <typename T, int TEAM, int NV, bool NT, bool TOKEN>
 __global__ __launch_bounds__(block_threads(TEAM)) void block_norm_backward_kernel(BlockNormBackwardArgs a) {
   constexpr int kTeams = block_threads(TEAM) / TEAM;
-  constexpr bool kAhead = TEAM * NV < 1024;                   // the next row fits in registers too
-  __shared__ float buf[2][6][TEAM / 64];
+  constexpr bool kAhead = TEAM < 1024 && (NV == 1 || sizeof(T) == 2 || !TOKEN);    // the next row fits in registers too
+  __shared__ float buf[2][6][waves_of(TEAM)];
   TeamSum<TEAM, 6> sum{buf};
-  const int team = __builtin_amdgcn_readfirstlane((int)blockIdx.x * kTeams + (kTeams > 1 ? (int)threadIdx.x / TEAM : 0));
-  if (team >= a.plan.teams) return;
+  const int team = own_team<TEAM>();
   const int64_t period = a.gate_rows;
-  const bool groups = !TOKEN && a.gate;
+  const bool groups = !TOKEN && a.gate, there = team < a.plan.teams;
   int64_t lo, hi, step = 1, group = 0;
-  if (a.plan.teams_per_group > 0) {            // every so many rows of a group
+  if (kTeams > 1 && !there) {
+    lo = hi = 0;
+  } else if (a.plan.teams_per_group > 0) {            // every so many rows of a group
     group = team / a.plan.teams_per_group;
     lo = group * period + team % a.plan.teams_per_group;
     hi = (group + 1) * period;
@@ -426,18 +466,37 @@ __global__ __launch_bounds__(block_threads(TEAM)) void block_norm_backward_kerne
     if constexpr (kAhead) q = next;
     else if (t + step < hi) load(q, t + step);
   }
-  const int64_t at = (int64_t)team * a.d;
-  if constexpr (!TOKEN)
-    leave(!groups ? nullptr : a.plan.teams_per_group ? a.part_gate + at : static_cast<float*>(a.dgate) + group * a.d);
+  const int64_t at = (int64_t)blockIdx.x * a.d;
+  const bool first = kTeams == 1 || threadIdx.x < TEAM;
+  if constexpr (kTeams == 1) {
+    if constexpr (!TOKEN)
+      leave(!groups ? nullptr : a.plan.teams_per_group ? a.part_gate + at : static_cast<float*>(a.dgate) + group * a.d);
+  } else {
+    __shared__ f32x4 teams[4][TEAM < 64 ? TEAM : 64][2];
+    if constexpr (!TOKEN) {
+      float* dgate = nullptr;
+      if (a.plan.teams_per_group == 0) {
+        if (groups && there) dgate = static_cast<float*>(a.dgate) + group * a.d;
+      } else if (a.plan.group_parts < a.plan.teams_per_group) {     // the workgroup's teams are of one group
+        join<TEAM>(P[0], teams);
+        if (first) dgate = a.part_gate + at;
+      } else if (there) {
+        dgate = a.part_gate + (int64_t)team * a.d;
+      }
+      leave(dgate);
+    }
+    if (post) join<TEAM>(acc_post[0], teams);
+    if (norm_next) join<TEAM>(acc_next[0], teams);
+  }
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    if (!p.in[i]) continue;
+    if (!p.in[i] || !first) continue;
     if (post) store8(a.part_post + at + p.col[i], acc_post[i]);
     if (norm_next) store8(a.part_next + at + p.col[i], acc_next[i]);
   }
 }
 
-// Column sums of the teams' parts, 64 columns a workgroup: 64 runs of teams, one for every
+// Column sums of the parts, 64 columns a workgroup: 64 runs of parts, one for every
 // 16 lanes of four columns each, then the runs in order.  blockIdx.y: the post gain, the next
 // gain (those that there are), then the gate groups whose rows several teams share.  (16
 // runs, a column a lane: 5.4 us for the two sums of 512 parts 1,024 wide, against 4.7.)
@@ -447,7 +506,7 @@ __global__ __launch_bounds__(16 * kRuns) void reduce_parts_kernel(BlockNormBackw
   int job = blockIdx.y;
   const float* part;
   float* dst;
-  int64_t first = 0, count = a.plan.teams;
+  int64_t first = 0, count = a.plan.parts;
   if (a.post_gain && job-- == 0) {
     part = a.part_post;
     dst = a.d_post_gain;
@@ -457,7 +516,7 @@ __global__ __launch_bounds__(16 * kRuns) void reduce_parts_kernel(BlockNormBackw
   } else {
     part = a.part_gate;
     dst = static_cast<float*>(a.dgate) + (int64_t)job * a.d;
-    count = a.plan.teams_per_group;
+    count = a.plan.group_parts;
     first = (int64_t)job * count;
   }
   const int lane = threadIdx.x & 15, run = threadIdx.x >> 4, c = (int)blockIdx.x * 64 + lane * 4;
@@ -483,16 +542,29 @@ __global__ __launch_bounds__(16 * kRuns) void reduce_parts_kernel(BlockNormBackw
   }
 }
 
-// The team that holds a row of d elements: eight a lane up to 8,192, then sixteen.
+// The team that holds a row of d elements: eight a lane up to 8,192, then sixteen.  (A whole
+// wavefront for rows of 64, seven eighths of it idle: 126,825 rows forward 46.1 us instead of
+// 14.1, 200,000 backward 128 instead of 36.)
 template <typename F> void by_width(int64_t d, F f) {
   using std::integral_constant;
-  if (d <= 512) f(integral_constant<int, 64>{}, integral_constant<int, 1>{});
+  if (d <= 64) f(integral_constant<int, 8>{}, integral_constant<int, 1>{});
+  else if (d <= 128) f(integral_constant<int, 16>{}, integral_constant<int, 1>{});
+  else if (d <= 256) f(integral_constant<int, 32>{}, integral_constant<int, 1>{});
+  else if (d <= 512) f(integral_constant<int, 64>{}, integral_constant<int, 1>{});
   else if (d <= 1024) f(integral_constant<int, 128>{}, integral_constant<int, 1>{});
   else if (d <= 2048) f(integral_constant<int, 256>{}, integral_constant<int, 1>{});
   else if (d <= 4096) f(integral_constant<int, 512>{}, integral_constant<int, 1>{});
   else if (d <= 6144) f(integral_constant<int, 768>{}, integral_constant<int, 1>{});
   else if (d <= 8192) f(integral_constant<int, 1024>{}, integral_constant<int, 1>{});
   else f(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
+}
+
+// The backward's: 1,024 threads may have 128 registers each, which it needs more than, so
+// up to 8,192 columns 512 threads have sixteen elements each (2,000 rows of 8,192 bf16 47.7 us,
+// 75.4 with 1,024 threads; 870 of 7,616 float32 44.3, 83.5).
+template <typename F> void by_width_backward(int64_t d, F f) {
+  if (d > 6144 && d <= 8192) f(std::integral_constant<int, 512>{}, std::integral_constant<int, 2>{});
+  else by_width(d, f);
 }
 
 // Rows go past the caches where one tensor of them is larger than what the caches hold of it
@@ -540,35 +612,56 @@ hipError_t launch_block_norm(int dtype, const BlockNormArgs& a, int num_cu, hipS
   return hipGetLastError();
 }
 
-// Teams of 12 wavefronts a CU on a card of 256 CUs (what their registers allow at once), but
-// two rows a team at least: each team writes one part of d floats a sum, which the second
-// kernel reads again (1,021 rows of 1,024 float32: one row a team 18.0 us, two 17.9, four 19.4).
+// Teams of 12 wavefronts a CU on a card of 256 CUs (what their registers allow at once).  Each
+// workgroup writes one part of d floats a sum, which the second kernel reads again, so two rows
+// a team at least (2,000 rows of 512 bf16: one row 11.0 us, two 9.6) unless that leaves half the
+// CUs without work (20 rows of 512: one 6.4, two 7.1), and one workgroup, whose part is the sum,
+// where two rows a team are enough for it (8 rows of 512: 4.8, two workgroups 6.4).
 RowPlan block_norm_row_plan(int64_t T, int64_t d, int64_t gate_rows) {
-  int64_t teams = 0;
-  by_width(d, [&](auto team, auto) {
-    constexpr int TEAM = decltype(team)::value, waves = TEAM / 64;
-    teams = 256 * (12 / waves > 0 ? 12 / waves : 1);
+  int64_t teams = 0, per = 1;                  // per: teams of a workgroup
+  by_width_backward(d, [&](auto team, auto) {
+    constexpr int TEAM = decltype(team)::value, waves = waves_of(TEAM);
+    per = block_threads(TEAM) / TEAM;
+    teams = 256 * (12 / waves > 0 ? 12 / waves : 1) * (TEAM < 64 ? 64 / TEAM : 1);
   });
   int64_t rows = (T + teams - 1) / teams;
-  if (rows < 2) rows = 2;
+  if (T <= 2 * per) rows = (T + per - 1) / per;
+  else if (rows < 2 && T > 128 * per) rows = 2;
   RowPlan p{};
-  if (gate_rows <= 1 || gate_rows <= rows) {
+  const int64_t groups = gate_rows > 1 ? (T + gate_rows - 1) / gate_rows : 0;
+  // a team's longest run of whole groups: narrow rows in many groups of a few rows more than a
+  // team's share stay in one team, without a sum over teams for each group
+  const int64_t whole = per > 4 && groups >= 1024 ? 4 * rows : rows;
+  if (gate_rows <= 1 || gate_rows <= whole) {
     if (gate_rows > 1) rows = (rows + gate_rows - 1) / gate_rows * gate_rows;
     p.rows = rows;
     p.teams = (int)((T + rows - 1) / rows);
   } else {
-    const int64_t groups = (T + gate_rows - 1) / gate_rows;
     const int64_t len = gate_rows < T ? gate_rows : T;     // rows of the longest group
-    p.teams_per_group = (int)((len + rows - 1) / rows);
-    p.rows = (len + p.teams_per_group - 1) / p.teams_per_group;
-    p.teams = (int)(groups * p.teams_per_group);
+    int64_t of_group = (len + rows - 1) / rows;
+    const bool joined = of_group >= per || groups == 1;    // whole workgroups of a group's teams
+    if (joined) of_group = (of_group + per - 1) / per * per;
+    p.teams_per_group = (int)of_group;
+    p.group_parts = (int)(joined ? of_group / per : of_group);
+    p.rows = (len + of_group - 1) / of_group;
+    p.teams = (int)(groups * of_group);
   }
+  p.parts = (int)((p.teams + per - 1) / per);
   return p;
 }
 
-hipError_t launch_block_norm_backward(int dtype, const BlockNormBackwardArgs& a, hipStream_t stream) {
+hipError_t launch_block_norm_backward(int dtype, const BlockNormBackwardArgs& args, hipStream_t stream) {
+  BlockNormBackwardArgs a = args;
+  const int64_t groups = a.plan.teams_per_group ? a.plan.teams / a.plan.teams_per_group : 0;
+  int64_t jobs = (a.post_gain != nullptr) + (a.next_gain != nullptr) + groups;
+  if (a.plan.parts == 1 && (groups == 0 || a.plan.group_parts == 1)) {   // a part is the sum
+    a.part_post = a.d_post_gain;
+    a.part_next = a.d_next_gain;
+    a.part_gate = static_cast<float*>(a.dgate);
+    jobs = 0;
+  }
   by_flags(past_caches(a.T, a.d, dtype), a.gate && a.gate_rows == 1, [&](auto nt, auto token) {
-    by_width(a.d, [&](auto team, auto nv) {
+    by_width_backward(a.d, [&](auto team, auto nv) {
       constexpr int TEAM = decltype(team)::value, NV = decltype(nv)::value;
       constexpr bool NT = decltype(nt)::value, TOKEN = decltype(token)::value;
       if (dtype == 1) launch_backward<bf16, TEAM, NV, NT, TOKEN>(a, stream);
@@ -577,8 +670,6 @@ hipError_t launch_block_norm_backward(int dtype, const BlockNormBackwardArgs& a,
   });
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
-  const int64_t groups = a.plan.teams_per_group ? a.plan.teams / a.plan.teams_per_group : 0;
-  const int64_t jobs = (a.post_gain != nullptr) + (a.next_gain != nullptr) + groups;
   if (jobs == 0) return hipSuccess;
   hipLaunchKernelGGL(reduce_parts_kernel, dim3((unsigned)(a.d / 64), (unsigned)jobs), dim3(16 * kRuns), 0, stream, a);
   return hipGetLastError();

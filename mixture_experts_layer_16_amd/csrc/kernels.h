@@ -123,10 +123,12 @@ hipError_t launch_block_norm(int dtype, const BlockNormArgs& a, int num_cu, hipS
 
 // How the backward deals rows to teams, `rows` each at most: with teams_per_group > 0 each
 // gate group has that many teams of its own; otherwise a team's rows are consecutive and
-// cover whole groups, or any without a group to share.
+// cover whole groups, or any without a group to share.  Teams of one workgroup add up their
+// column sums before these go out: `parts` rows of each in all, and group_parts of the gate's
+// for each group (as many as its teams, where teams of other groups are in their workgroups).
 struct RowPlan {
-  int teams;
-  int teams_per_group;
+  int teams, teams_per_group;
+  int parts, group_parts;
   int64_t rows;
 };
 RowPlan block_norm_row_plan(int64_t T, int64_t d, int64_t gate_rows);
@@ -140,7 +142,7 @@ struct BlockNormBackwardArgs {
   float res_scale, branch_scale, eps;
   void *dx, *dy, *dgate;
   float *d_post_gain, *d_next_gain;
-  float *part_post, *part_next, *part_gate;   // [teams, d] each
+  float *part_post, *part_next, *part_gate;   // [parts, d], [parts, d], [groups, group_parts, d]
   RowPlan plan;
 };
 hipError_t launch_block_norm_backward(int dtype, const BlockNormBackwardArgs& a, hipStream_t stream);

@@ -558,11 +558,14 @@ moe_status moe_block_norm_backward(int64_t T, int64_t d, moe_dtype dtype, const 
   if (st != MOE_OK) return st;
   moe::BlockNormBackwardArgs a{};
   a.plan = moe::block_norm_row_plan(T, d, gate ? gate_rows : 0);
-  const size_t part = (size_t)a.plan.teams * (size_t)d * 4;
+  const size_t row = (size_t)d * 4, part = (size_t)a.plan.parts * row;
   Carver c(ws);
   a.part_post = post_gain ? static_cast<float*>(c.take(part)) : nullptr;
   a.part_next = next_gain ? static_cast<float*>(c.take(part)) : nullptr;
-  a.part_gate = a.plan.teams_per_group ? static_cast<float*>(c.take(part)) : nullptr;
+  if (a.plan.teams_per_group > 0) {
+    const size_t groups = (size_t)(a.plan.teams / a.plan.teams_per_group);
+    a.part_gate = static_cast<float*>(c.take(groups * (size_t)a.plan.group_parts * row));
+  }
   if (ws == nullptr && ws_bytes != nullptr) {
     *ws_bytes = c.used;
     return MOE_OK;

@@ -120,4 +120,22 @@ __device__ __forceinline__ float wave_total(float v) {
   return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
 
+// Sums over LANES lanes next to one another (8, 16, 32: each such group its own, with the
+// others' lanes on or off; 64: wave_total).  Each step adds a lane's mirror image, so all
+// lanes end with the same bits.
+template <int LANES> __device__ __forceinline__ float lanes_total(float v) {
+  if constexpr (LANES == 64) {
+    return wave_total(v);
+  } else {
+#define MOE_SUM_STEP(ctrl) v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), ctrl, 0xf, 0xf, false))
+    MOE_SUM_STEP(0xb1);                          // quad_perm 1,0,3,2
+    MOE_SUM_STEP(0x4e);                          // quad_perm 2,3,0,1
+    MOE_SUM_STEP(0x141);                         // row_half_mirror: the eight lanes' two quads
+    if (LANES > 8) MOE_SUM_STEP(0x140);          // row_mirror: the sixteen's two halves
+#undef MOE_SUM_STEP
+    if (LANES > 16) v += __shfl_xor(v, 16, 64);
+    return v;
+  }
+}
+
 }  // namespace moe

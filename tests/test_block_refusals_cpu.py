@@ -72,10 +72,15 @@ def test_block_norm_backward_refuses(want, kw):
 
 
 def test_block_norm_backward_workspace():
-    # one part of d floats for a team and sum; two rows a team at least, and 12 wavefronts' teams for
-    # 256 CUs at most: 3,072 (d <= 512), 1,536 (<= 1,024), 768 (<= 2,048)
-    assert back(query=True) == (OK, 2 * 4 * 128 * 4)
-    assert back(query=True, next_gain=None) == (OK, 4 * 128 * 4)
+    # one part of d floats for a workgroup and sum; two rows a team at least (one, where 128 workgroups
+    # then do), and 12 wavefronts' teams for 256 CUs at most: 24,576 (d <= 64, 32 a workgroup), 12,288 (<= 128, 16), 6,144 (<= 256, 8),
+    # 3,072 (<= 512, 4), 1,536 (<= 1,024, 1 as from here on), 768 (<= 2,048)
+    assert back(query=True) == (OK, 2 * 1 * 128 * 4)
+    assert back(query=True, next_gain=None) == (OK, 1 * 128 * 4)
+    assert back(query=True, T=2, d=1024) == (OK, 2 * 1 * 1024 * 4)
+    assert back(query=True, T=3, d=1024) == (OK, 2 * 3 * 1024 * 4)
+    assert back(query=True, T=128, d=1024) == (OK, 2 * 128 * 1024 * 4)
+    assert back(query=True, T=129, d=1024) == (OK, 2 * 65 * 1024 * 4)
     assert back(query=True, post_gain=None, next_gain=None) == (OK, 0)
     assert back(query=True, T=4096, d=1024) == (OK, 2 * 1366 * 1024 * 4)
     assert back(query=True, T=4096, d=1088) == (OK, 2 * 683 * 1088 * 4)
@@ -83,6 +88,12 @@ def test_block_norm_backward_workspace():
     assert back(query=True, T=4096, d=1088, gate=P, gate_rows=2048) == (OK, 3 * 684 * 1088 * 4)
     # groups of 4 rows: 8 rows a team, no parts of the gate
     assert back(query=True, T=4096, d=1088, gate=P, gate_rows=4) == (OK, 2 * 512 * 1088 * 4)
+    # narrow rows, 9 a team: 22,223 teams; groups of 36 are still a team's; groups of 100 have 12
+    # teams with parts of their own, groups of 5,963 have 663, made 21 workgroups, with one each
+    assert back(query=True, T=200000, d=64) == (OK, 2 * 695 * 64 * 4)
+    assert back(query=True, T=200000, d=64, gate=P, gate_rows=36) == (OK, 2 * 174 * 64 * 4)
+    assert back(query=True, T=200000, d=64, gate=P, gate_rows=100) == (OK, (2 * 750 + 24000) * 64 * 4)
+    assert back(query=True, T=200000, d=64, gate=P, gate_rows=5963) == (OK, (2 * 714 + 714) * 64 * 4)
 
 
 def w4(fn, **kw):

@@ -116,7 +116,7 @@ def run_case(T, d, dt, branch, post, gate_rows, act, nxt, seed=0):
             check(g, *want[name], g.dtype, name, 0 if rows else T)
 
 
-WIDTHS = [64, 192, 512, 576, 1024, 1088, 2048, 2112, 4096, 4160, 6144, 6208, 8192, 8256, 16384]
+WIDTHS = [64, 128, 192, 256, 320, 512, 576, 1024, 1088, 2048, 2112, 4096, 4160, 6144, 6208, 8192, 8256, 16384]
 
 
 @pytest.mark.parametrize("dt", [BF, FP])
@@ -144,8 +144,30 @@ def test_every_combination(branch, post, gate_rows, act, nxt):
 
 @pytest.mark.parametrize("gate_rows", [1, 2, 3, 7, 700, 1699, 5999, 6000, 6001, 10 ** 12])
 def test_gate_groups_over_many_teams(gate_rows):
-    # narrow rows: 3 rows a team, so groups lie inside, straddle and span teams
+    # narrow rows, a few a team: groups lie inside, straddle and span teams
     run_case(6000, 64, BF, "y", True, gate_rows, "tanh", True, seed=9)
+
+
+@pytest.mark.parametrize("dt", [BF, FP])
+@pytest.mark.parametrize("gate_rows", [0, 1, 5, 9, 31, 65, 200, 4001])
+@pytest.mark.parametrize("d", [64, 128, 256, 448, 512])
+def test_several_teams_a_wavefront(d, gate_rows, dt):
+    # teams of 8 to 64 lanes; workgroups whose teams share a gate group, and that do not, and a
+    # last one with teams that have no rows
+    run_case(4001, d, dt, "y", True, gate_rows, "tanh" if gate_rows else "none", True, seed=d + gate_rows)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("T", [1, 2, 63, 300])
+def test_several_teams_a_wavefront_from_expert_rows(T, d):
+    run_case(T, d, BF, 3, True, 7, "sigmoid", True, seed=T)
+
+
+@pytest.mark.parametrize("d", [64, 192, 512])
+def test_narrow_rows_past_the_caches(d):
+    # more than 32 MB a tensor, and more rows than teams
+    T = (33 << 20) // (2 * d) + 5
+    run_case(T, d, BF, "y", True, 1000, "sigmoid", True, seed=d)
 
 
 @pytest.mark.parametrize("gate_rows", [3, 130, 1500])
