@@ -486,8 +486,9 @@ moe_status moe_w4_dequantize(int64_t n, int64_t R, int64_t C, moe_dtype dtype, i
 /*
  * moe_w4_matvec: y [T,R] = x [T,C] W^T for one 4-bit matrix and few tokens (each
  * weight is read once for every 16 tokens).  x and y in dtype; products and sums are
- * float32 (float32 x enters with all its bits).  |x| of 1e34 and above, infinities and
- * NaN make their own token's y NaN; other tokens are not touched.
+ * float32 (float32 x enters with all its bits).  Infinities and NaN, and |x| of 1e34 and
+ * above, can make their own token's y NaN; other tokens are not touched.  y must not
+ * overlap x.
  *   ws: query with ws == NULL (float32 x: 6 T C bytes, else 0)
  * Errors as moe_w4_pack; MOE_ERR_UNSUPPORTED also for T above 2^19 and for more than
  * 2^24 pairs of 16 rows of x and 16 rows of W, and for x of 2^31 elements (float32: a

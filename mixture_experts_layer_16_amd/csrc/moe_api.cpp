@@ -150,6 +150,13 @@ void carve_route_backward(Carver& c, moe::RouteBackwardScratch& w, int64_t T, in
 constexpr int64_t kMaxNormDim = 16384;
 
 // The checks that the block norm's two directions share.
+// A group of more rows than there are is a group of all of them (of two and more: a row of its
+// own for a token is another case, whose dgate has another type).
+int64_t one_group(int64_t gate_rows, int64_t T) {
+  const int64_t most = T < 2 ? 2 : T;
+  return gate_rows < most ? gate_rows : most;
+}
+
 moe_status check_block_norm(int64_t T, int64_t d, moe_dtype dtype, const void* gate, int64_t gate_rows,
                             moe_gate_act gate_act, float eps) {
   if (T <= 0 || d <= 0 || !(eps >= 0.0f)) return MOE_ERR_INVALID_ARG;
@@ -543,7 +550,7 @@ moe_status moe_block_norm(int64_t T, int64_t d, int64_t k, moe_dtype dtype, cons
   a.x = x; a.y = y; a.y_perm = y_perm; a.slot_row = slot_row; a.topk_w = topk_w;
   a.has_y = branch;
   a.post_gain = post_gain; a.next_gain = next_gain;
-  a.gate = gate; a.gate_rows = gate_rows; a.gate_act = gate_act;
+  a.gate = gate; a.gate_rows = one_group(gate_rows, T); a.gate_act = gate_act;
   a.res_scale = res_scale; a.branch_scale = branch_scale; a.eps = eps;
   a.out = out; a.h = h; a.y_out = y_out;
   return hip_status(moe::launch_block_norm(dtype, a, ncu, static_cast<hipStream_t>(stream)));
@@ -556,6 +563,7 @@ moe_status moe_block_norm_backward(int64_t T, int64_t d, moe_dtype dtype, const 
                                    void* dgate, float* d_next_gain, void* ws, size_t* ws_bytes, void* stream) {
   moe_status st = check_block_norm(T, d, dtype, gate, gate_rows, gate_act, eps);
   if (st != MOE_OK) return st;
+  gate_rows = one_group(gate_rows, T);
   moe::BlockNormBackwardArgs a{};
   a.plan = moe::block_norm_row_plan(T, d, gate ? gate_rows : 0);
   const size_t row = (size_t)d * 4, part = (size_t)a.plan.parts * row;
@@ -631,7 +639,7 @@ moe_status moe_w4_matvec(int64_t T, int64_t C, int64_t R, moe_dtype dtype, int64
     *ws_bytes = need;
     return MOE_OK;
   }
-  if (!ok16(x) || !ok16(codes) || !ok16(scales) || !ok16(y)) return MOE_ERR_INVALID_ARG;
+  if (!ok16(x) || !ok16(codes) || !ok16(scales) || !ok16(y) || y == x) return MOE_ERR_INVALID_ARG;
   if (workspace_step(ws, ws_bytes, need, &st)) return st;
   int ncu = 0;
   if ((st = num_cu(&ncu)) != MOE_OK) return st;

@@ -10,6 +10,7 @@ from mixture_experts_layer_16_amd import binding as B
 
 OK, INVALID, UNSUPPORTED, WORKSPACE = 0, 1, 2, 3
 P = ctypes.c_void_p(0x10000)
+Y = ctypes.c_void_p(1 << 21)
 MIS = ctypes.c_void_p(0x10002)
 
 
@@ -86,6 +87,10 @@ def test_block_norm_backward_workspace():
     assert back(query=True, T=4096, d=1088) == (OK, 2 * 683 * 1088 * 4)
     # 2,048 rows a gate group, 6 rows a team: 342 teams a group and their own parts
     assert back(query=True, T=4096, d=1088, gate=P, gate_rows=2048) == (OK, 3 * 684 * 1088 * 4)
+    # one group, of T rows or any number above
+    for rows in (4096, 4097, 2 ** 63 - 1):
+        assert back(query=True, T=4096, d=1088, gate=P, gate_rows=rows) == (OK, 3 * 683 * 1088 * 4)
+    assert back(query=True, T=1, gate=P, gate_rows=2 ** 63 - 1) == back(query=True, T=1, gate=P, gate_rows=2)
     # groups of 4 rows: 8 rows a team, no parts of the gate
     assert back(query=True, T=4096, d=1088, gate=P, gate_rows=4) == (OK, 2 * 512 * 1088 * 4)
     # narrow rows, 9 a team: 22,223 teams; groups of 36 are still a team's; groups of 100 have 12
@@ -122,7 +127,7 @@ def test_w4_layout_calls_refuse_their_own():
 
 def matvec(**kw):
     n = ctypes.c_size_t(1 << 40)
-    a = dict(T=3, C=128, R=64, dtype=0, group=128, x=P, codes=P, scales=P, y=P, ws=P, n=ctypes.byref(n), stream=None)
+    a = dict(T=3, C=128, R=64, dtype=0, group=128, x=P, codes=P, scales=P, y=Y, ws=P, n=ctypes.byref(n), stream=None)
     a.update(kw)
     return B.lib().moe_w4_matvec(*a.values()), n.value
 
@@ -131,7 +136,7 @@ def matvec(**kw):
     (INVALID, dict(T=0)), (INVALID, dict(R=0)), (UNSUPPORTED, dict(C=48)), (UNSUPPORTED, dict(group=256)),
     (UNSUPPORTED, dict(dtype=3)), (UNSUPPORTED, dict(T=(1 << 19) + 1)), (UNSUPPORTED, dict(T=1 << 19, R=8192)),
     (UNSUPPORTED, dict(T=1 << 15, C=1 << 20)), (UNSUPPORTED, dict(T=1 << 11, C=1 << 20, dtype=1)), (INVALID, dict(x=None)), (INVALID, dict(x=MIS)),
-    (INVALID, dict(codes=MIS)), (INVALID, dict(scales=None)), (INVALID, dict(y=None)), (INVALID, dict(ws=MIS)),
+    (INVALID, dict(codes=MIS)), (INVALID, dict(scales=None)), (INVALID, dict(y=None)), (INVALID, dict(y=P)), (INVALID, dict(ws=MIS)),
     (WORKSPACE, dict(ws=None, n=None)), (WORKSPACE, dict(n=ctypes.byref(ctypes.c_size_t(64))))])
 def test_matvec_refuses(want, kw):
     assert matvec(**kw)[0] == want

@@ -142,7 +142,7 @@ def test_every_combination(branch, post, gate_rows, act, nxt):
     run_case(41, 576, BF, branch, post, gate_rows, act, nxt, seed=3)
 
 
-@pytest.mark.parametrize("gate_rows", [1, 2, 3, 7, 700, 1699, 5999, 6000, 6001, 10 ** 12])
+@pytest.mark.parametrize("gate_rows", [1, 2, 3, 7, 700, 1699, 5999, 6000, 6001, 10 ** 12, 2 ** 63 - 1])
 def test_gate_groups_over_many_teams(gate_rows):
     # narrow rows, a few a team: groups lie inside, straddle and span teams
     run_case(6000, 64, BF, "y", True, gate_rows, "tanh", True, seed=9)
@@ -234,8 +234,9 @@ def test_over_the_input(dt):
         assert bits_equal(getattr(b, name), getattr(want, name)), name
 
 
-def test_rows_of_zeros_and_of_nan_stay_theirs():
-    v, d_out, dh = draw(6, 576, BF, "y", True, 0, True, seed=6)
+@pytest.mark.parametrize("d", [64, 128, 256, 576])       # 64 to 256: rows that share a wavefront
+def test_rows_of_zeros_and_of_nan_stay_theirs(d):
+    v, d_out, dh = draw(6, d, BF, "y", True, 0, True, seed=6)
     clean = forward(v)
     w = dict(v, x=v["x"].clone(), y=v["y"].clone())
     w["y"][1] = 0
