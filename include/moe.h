@@ -1,6 +1,7 @@
 /*
  * moe.h - C ABI of the MI355X (gfx950) routed Mixture-of-Experts layer: forward,
- * backward, and Muon's Newton-Schulz step for whole expert matrices.
+ * backward, Muon's Newton-Schulz step for whole expert matrices, the norms around
+ * the block, and experts with 4-bit weights.
  *
  * The layer (one Mixture-of-Experts block of the ~1T-parameter model in
  * "Training a 1T-Parameter MoE on EU public infrastructure with PyTorch and

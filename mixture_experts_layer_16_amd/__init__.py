@@ -1,4 +1,4 @@
-"""MI355X (gfx950) routed Mixture-of-Experts layer forward.
+"""MI355X (gfx950) routed Mixture-of-Experts layer, the norms around its block and 4-bit experts.
 
 The compute path is libmoe.so (hand-written HIP kernels behind a C ABI, see
 include/moe.h); `binding` marshals torch device tensors into it and

@@ -568,7 +568,8 @@ template <typename F> void by_width_backward(int64_t d, F f) {
 }
 
 // Rows go past the caches where one tensor of them is larger than what the caches hold of it
-// anyway (4 MB of L2 an XCD): 32 MB.
+// anyway (4 MB of L2 an XCD): 32 MB (32,768 rows of 6,144 bf16 290 us, 311 through them; 2,000
+// such rows, 25 MB, 21.0 and 20.5 past them).
 bool past_caches(int64_t T, int64_t d, int dtype) { return T * d * (dtype == 1 ? 2 : 4) >= (int64_t(32) << 20); }
 
 template <typename T, int TEAM, int NV, bool NT, bool TOKEN>
