@@ -496,13 +496,13 @@ __global__ __launch_bounds__(block_threads(TEAM)) void block_norm_backward_kerne
   }
 }
 
-// Column sums of the parts, 64 columns a workgroup: 64 runs of parts, one for every
-// 16 lanes of four columns each, then the runs in order.  blockIdx.y: the post gain, the next
-// gain (those that there are), then the gate groups whose rows several teams share.  (16
-// runs, a column a lane: 5.4 us for the two sums of 512 parts 1,024 wide, against 4.7.)
-constexpr int kRuns = 64;
-__global__ __launch_bounds__(16 * kRuns) void reduce_parts_kernel(BlockNormBackwardArgs a) {
-  __shared__ f32x4 buf[kRuns][16];
+// Column sums of the parts: runs of parts, one for every LANES lanes of four columns each, then
+// the runs in order.  blockIdx.y: the post gain, the next gain (those that there are), then the
+// gate groups whose rows several workgroups share.  64 columns a workgroup and 64 runs, or 32
+// and 128 where that leaves the card with few workgroups of many parts each (launch_reduce).
+template <int LANES> __global__ __launch_bounds__(1024) void reduce_parts_kernel(BlockNormBackwardArgs a) {
+  constexpr int kRuns = 1024 / LANES;
+  __shared__ f32x4 buf[kRuns][LANES];
   int job = blockIdx.y;
   const float* part;
   float* dst;
@@ -519,7 +519,7 @@ __global__ __launch_bounds__(16 * kRuns) void reduce_parts_kernel(BlockNormBackw
     count = a.plan.group_parts;
     first = (int64_t)job * count;
   }
-  const int lane = threadIdx.x & 15, run = threadIdx.x >> 4, c = (int)blockIdx.x * 64 + lane * 4;
+  const int lane = threadIdx.x % LANES, run = threadIdx.x / LANES, c = ((int)blockIdx.x * LANES + lane) * 4;
   const int64_t per = (count + kRuns - 1) / kRuns;
   const int64_t lo = first + run * per, hi = lo + per < first + count ? lo + per : first + count;
   f32x4 v = {0.f, 0.f, 0.f, 0.f};
@@ -527,11 +527,11 @@ __global__ __launch_bounds__(16 * kRuns) void reduce_parts_kernel(BlockNormBackw
   for (int64_t w = lo; w < hi; ++w) v += *reinterpret_cast<const f32x4*>(part + w * a.d + c);
   buf[run][lane] = v;
   __syncthreads();
-  __shared__ f32x4 eight[8][16];
+  __shared__ f32x4 eight[8][LANES];
   if (run < 8) {
-    v = buf[run * 8][lane];
+    v = buf[run * (kRuns / 8)][lane];
 #pragma unroll
-    for (int q = 1; q < 8; ++q) v += buf[run * 8 + q][lane];
+    for (int q = 1; q < kRuns / 8; ++q) v += buf[run * (kRuns / 8) + q][lane];
     eight[run][lane] = v;
   }
   __syncthreads();
@@ -589,6 +589,16 @@ void launch_backward(const BlockNormBackwardArgs& a, hipStream_t stream) {
   constexpr int threads = block_threads(TEAM), per = threads / TEAM;
   const dim3 grid((unsigned)((a.plan.teams + per - 1) / per)), block(threads);
   hipLaunchKernelGGL((block_norm_backward_kernel<T, TEAM, NV, NT, TOKEN>), grid, block, 0, stream, a);
+}
+
+// With a launch: the two sums of 511 parts 1,024 wide by 32 columns 14.9 us for the whole call,
+// by 64 16.7 (a column a lane and 16 runs: 0.7 more); sums over 2,000 gate groups of 12 parts
+// 64 wide 48.8 and 43.3; few parts leave the 128 runs idle.
+void launch_reduce(const BlockNormBackwardArgs& a, int64_t jobs, hipStream_t stream) {
+  const bool narrow = a.d / 64 * jobs <= 128 && a.plan.parts >= 128;
+  const dim3 grid((unsigned)(a.d / (narrow ? 32 : 64)), (unsigned)jobs), block(1024);
+  if (narrow) hipLaunchKernelGGL(reduce_parts_kernel<8>, grid, block, 0, stream, a);
+  else hipLaunchKernelGGL(reduce_parts_kernel<16>, grid, block, 0, stream, a);
 }
 
 // f(nt, token) with both as types
@@ -672,7 +682,7 @@ hipError_t launch_block_norm_backward(int dtype, const BlockNormBackwardArgs& ar
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
   if (jobs == 0) return hipSuccess;
-  hipLaunchKernelGGL(reduce_parts_kernel, dim3((unsigned)(a.d / 64), (unsigned)jobs), dim3(16 * kRuns), 0, stream, a);
+  launch_reduce(a, jobs, stream);
   return hipGetLastError();
 }
 
