@@ -527,13 +527,20 @@ class W4Weights:
             raise MoEError("4-bit weights", 2)
         self.n, self.R, self.C, self.group = n, R, C, group
         row_tiles, col_tiles = n * -(-R // 16), -(-C // 128)
-        self.codes = torch.empty(row_tiles * col_tiles * 1024, dtype=torch.uint8, device=dev)
+        self._codes = torch.empty(row_tiles * col_tiles * 1024, dtype=torch.uint8, device=dev)
         row_scales = -(-col_tiles * (128 // group) // 4) * 4
-        self.scales = torch.empty(row_tiles * 16 * row_scales, dtype=torch.bfloat16, device=dev)
+        self._scales = torch.empty(row_tiles * 16 * row_scales, dtype=torch.bfloat16, device=dev)
+        self.device = self._codes.device
+        self._sizes = (_i64(n), _i64(R), _i64(C))
+        self._layout = (_i64(group), _p(self._codes), _p(self._scales))
 
     @property
-    def device(self):
-        return self.codes.device
+    def codes(self):
+        return self._codes
+
+    @property
+    def scales(self):
+        return self._scales
 
     def dequantize(self, dtype=torch.bfloat16, out=None):
         """The values [n, R, C] that the codes and scales stand for, rounded once to dtype."""
@@ -541,8 +548,7 @@ class W4Weights:
         if out is None:
             out = torch.empty(self.n, self.R, self.C, dtype=dtype, device=dev)
         _same("out", out, dev, out.dtype, (self.n, self.R, self.C))
-        _launch("moe_w4_dequantize", dev, (self.n, self.R, self.C, dtype_code(out.dtype), self.group, _p(self.codes),
-                                           _p(self.scales), _p(out)))
+        _launch("moe_w4_dequantize", dev, (*self._sizes, dtype_code(out.dtype), *self._layout, out.data_ptr()))
         return out
 
 
