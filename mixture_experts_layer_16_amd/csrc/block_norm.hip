@@ -544,7 +544,9 @@ template <int LANES> __global__ __launch_bounds__(1024) void reduce_parts_kernel
 
 // The team that holds a row of d elements: eight a lane up to 8,192, then sixteen.  (A whole
 // wavefront for rows of 64, seven eighths of it idle: 126,825 rows forward 46.1 us instead of
-// 14.1, 200,000 backward 128 instead of 36.)
+// 14.1, 200,000 backward 128 instead of 36.  512 threads for rows of 2,496: 19,127 backward
+// 148 us, 384 threads 114, forward 80.4 and 79.5; 768 for 4,992: as fast as 640 backward, and
+// 109 us against 121 for 16,000 forward.)
 template <typename F> void by_width(int64_t d, F f) {
   using std::integral_constant;
   if (d <= 64) f(integral_constant<int, 8>{}, integral_constant<int, 1>{});
@@ -552,7 +554,9 @@ template <typename F> void by_width(int64_t d, F f) {
   else if (d <= 256) f(integral_constant<int, 32>{}, integral_constant<int, 1>{});
   else if (d <= 512) f(integral_constant<int, 64>{}, integral_constant<int, 1>{});
   else if (d <= 1024) f(integral_constant<int, 128>{}, integral_constant<int, 1>{});
+  else if (d <= 1536) f(integral_constant<int, 192>{}, integral_constant<int, 1>{});
   else if (d <= 2048) f(integral_constant<int, 256>{}, integral_constant<int, 1>{});
+  else if (d <= 384 * 8) f(integral_constant<int, 384>{}, integral_constant<int, 1>{});
   else if (d <= 4096) f(integral_constant<int, 512>{}, integral_constant<int, 1>{});
   else if (d <= 6144) f(integral_constant<int, 768>{}, integral_constant<int, 1>{});
   else if (d <= 8192) f(integral_constant<int, 1024>{}, integral_constant<int, 1>{});

@@ -74,8 +74,9 @@ def test_block_norm_backward_refuses(want, kw):
 
 def test_block_norm_backward_workspace():
     # one part of d floats for a workgroup and sum; two rows a team at least (one, where 128 workgroups
-    # then do), and 12 wavefronts' teams for 256 CUs at most: 24,576 (d <= 64, 32 a workgroup), 12,288 (<= 128, 16), 6,144 (<= 256, 8),
-    # 3,072 (<= 512, 4), 1,536 (<= 1,024, 1 as from here on), 768 (<= 2,048)
+    # then do), and 12 wavefronts' teams for 256 CUs at most: 24,576 (d <= 64, 32 a workgroup), 12,288
+    # (<= 128, 16), 6,144 (<= 256, 8), half of it (<= 512, 4), 1,536 (<= 1,024, 1 as from here on),
+    # 1,024 (<= 1,536), 768 (<= 2,048)
     assert back(query=True) == (OK, 2 * 1 * 128 * 4)
     assert back(query=True, next_gain=None) == (OK, 1 * 128 * 4)
     assert back(query=True, T=2, d=1024) == (OK, 2 * 1 * 1024 * 4)
@@ -84,15 +85,16 @@ def test_block_norm_backward_workspace():
     assert back(query=True, T=129, d=1024) == (OK, 2 * 65 * 1024 * 4)
     assert back(query=True, post_gain=None, next_gain=None) == (OK, 0)
     assert back(query=True, T=4096, d=1024) == (OK, 2 * 1366 * 1024 * 4)
-    assert back(query=True, T=4096, d=1088) == (OK, 2 * 683 * 1088 * 4)
+    assert back(query=True, T=4096, d=2048) == (OK, 2 * 683 * 2048 * 4)
     # 2,048 rows a gate group, 6 rows a team: 342 teams a group and their own parts
-    assert back(query=True, T=4096, d=1088, gate=P, gate_rows=2048) == (OK, 3 * 684 * 1088 * 4)
+    assert back(query=True, T=4096, d=2048, gate=P, gate_rows=2048) == (OK, 3 * 684 * 2048 * 4)
+    assert back(query=True, T=4096, d=1088) == (OK, 2 * 1024 * 1088 * 4)
     # one group, of T rows or any number above
     for rows in (4096, 4097, 2 ** 63 - 1):
-        assert back(query=True, T=4096, d=1088, gate=P, gate_rows=rows) == (OK, 3 * 683 * 1088 * 4)
+        assert back(query=True, T=4096, d=2048, gate=P, gate_rows=rows) == (OK, 3 * 683 * 2048 * 4)
     assert back(query=True, T=1, gate=P, gate_rows=2 ** 63 - 1) == back(query=True, T=1, gate=P, gate_rows=2)
     # groups of 4 rows: 8 rows a team, no parts of the gate
-    assert back(query=True, T=4096, d=1088, gate=P, gate_rows=4) == (OK, 2 * 512 * 1088 * 4)
+    assert back(query=True, T=4096, d=2048, gate=P, gate_rows=4) == (OK, 2 * 512 * 2048 * 4)
     # narrow rows, 9 a team: 22,223 teams; groups of 36 are still a team's; groups of 100 have 12
     # teams with parts of their own, groups of 5,963 have 663, made 21 workgroups, with one each
     assert back(query=True, T=200000, d=64) == (OK, 2 * 695 * 64 * 4)

@@ -116,7 +116,7 @@ def run_case(T, d, dt, branch, post, gate_rows, act, nxt, seed=0):
             check(g, *want[name], g.dtype, name, 0 if rows else T)
 
 
-WIDTHS = [64, 128, 192, 256, 320, 512, 576, 1024, 1088, 2048, 2112, 4096, 4160, 6144, 6208, 8192, 8256, 16384]
+WIDTHS = [64, 128, 192, 256, 320, 512, 576, 1024, 1088, 1536, 1600, 2048, 2112, 2496, 3136, 4096, 4160, 6144, 6208, 8192, 8256, 16384]
 
 
 @pytest.mark.parametrize("dt", [BF, FP])
